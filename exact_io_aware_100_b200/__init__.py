@@ -7,7 +7,8 @@ calls raise.
 
 Low-level names mirror the C ABI (``fa_fwd``, ``fa_fwd_ex``, ``fa_bwd``, ...)
 and take torch tensors for the pointer arguments.  ``forward`` / ``backward``
-allocate the outputs (and workspace) with torch and call them.
+allocate the outputs (and workspace) with torch and call them.  Rotary positions, the
+paged key/value cache and its pages are in ``serving`` and re-exported here.
 """
 from __future__ import annotations
 
@@ -25,6 +26,8 @@ EXPORTS = (
     "fa_fwd", "fa_fwd_ex", "fa_fwd_workspace_size", "fa_bwd", "fa_bwd_workspace_size",
     "fa_bwd_prepare", "fa_bwd_main", "fa_bwd_finish", "fa_bwd_noalloc", "fa_fwd_gqa", "fa_bwd_gqa",
     "fa_decode", "fa_decode_workspace_size", "fa_fwd_general", "fa_bwd_general", "fa_bwd_general_workspace_size",
+    "fa_rotary", "fa_paged_append", "fa_paged_decode", "fa_paged_decode_workspace_size", "fa_pages_workspace_size",
+    "fa_pages_extend", "fa_pages_fork", "fa_pages_free", "fa_pages_compact", "fa_pages_copy",
     "fa_get_device_status", "fa_selftest_wait_timeout", "fa_status_string", "fa_version",
 )
 
@@ -91,6 +94,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "fa_fwd_gqa", "fa_bwd_gqa", "fa_decode", "fa_fwd_general", "fa_bwd_general",
                  "fa_get_device_status", "fa_selftest_wait_timeout"):
         getattr(L, name).restype = I
+    serving.declare(L)
     _lib = L
     return L
 
@@ -429,3 +433,12 @@ def backward_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqle
         workspace = _workspace(fa_bwd_general_workspace_size(L), q.device)
     fa_bwd_general(q, k, v, o, lse, dout, dq, dk, dv, L, causal, workspace, scale, stream)
     return dq, dk, dv
+
+
+# ----------------------------------------------------------------- serving operators
+from . import serving                                                       # noqa: E402
+from .serving import (FaPagedLayout, FaPagesLayout, FaRotaryLayout,         # noqa: E402,F401
+                      fa_paged_append, fa_paged_decode, fa_paged_decode_workspace_size, fa_pages_compact, fa_pages_copy,
+                      fa_pages_extend, fa_pages_fork, fa_pages_free, fa_pages_workspace_size, fa_rotary, paged_append,
+                      paged_decode, pages_compact, pages_copy, pages_extend, pages_fork, pages_free, rotary,
+                      rotary_backward, rotary_frequencies)

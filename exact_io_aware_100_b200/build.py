@@ -13,8 +13,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa.so")
-SOURCES = ["fa_api.cu"]
-DEPS = ["fa_api.cu", "fwd_kernel.cuh", "bwd_kernel.cuh", "bwd256_kernel.cuh", "decode_kernel.cuh", "decode_warp_kernel.cuh", "fwd64_kernel.cuh", "fwd256_kernel.cuh", "layout.cuh", "ptx.cuh"]
+SOURCES = ["fa_lib.cu"]
+DEPS = ["fa_lib.cu", "fa_api.cu", "serving_api.cuh", "rotary_kernel.cuh", "paged_decode_kernel.cuh", "pages_kernel.cuh",
+        "fwd_kernel.cuh", "bwd_kernel.cuh", "bwd256_kernel.cuh", "decode_kernel.cuh", "decode_warp_kernel.cuh", "fwd64_kernel.cuh", "fwd256_kernel.cuh", "layout.cuh",
+        "ptx.cuh"]
 
 
 def nvcc_path() -> str:

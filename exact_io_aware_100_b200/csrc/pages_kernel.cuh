@@ -1,0 +1,315 @@
+// Bookkeeping of a paged cache's pages, and the copies that follow from it.
+//
+// The state is three int32 arrays (page tables, lengths, reference counts); a page is free when nobody holds
+// it, so there is no free list to keep in order: allocation ranks the free pages with a prefix sum over the
+// reference counts and hands them out lowest first, in the order of the requests.  That makes every result a
+// function of the state alone.  The work is a few hundred KB of integers: bound by latency, not by bandwidth, hence
+// one block that ranks and decides, with every read spread over its threads.
+#pragma once
+
+#include "layout.cuh"
+
+namespace fa {
+
+struct PagesArgs {
+  int* table;
+  long long table_stride;
+  int* lens;
+  int* refs;
+  int S, P, page, M;
+  int n;                           // requests
+  const int* seqs;                 // extend, free: sequences; fork: sources
+  const int* arg;                  // extend: tokens; fork: destinations
+  int* copies;
+  int* status;
+  int* claim;                      // workspace: [S] first request that names the sequence
+  int* snap;                       // workspace: [n] what a request asks for, by the state before the call; -1: refused
+  int* prefix;                     // workspace: [n] pages wanted by the requests before
+  int* list;                       // workspace: [P] free pages in order (extend, fork); new places (compact)
+  int* info;                       // workspace: [1] pages in use (compact)
+  uint32_t* dev_status;
+};
+
+constexpr int kPagesThreads = 1024;
+constexpr int kPagesPer = 8;       // consecutive values a thread takes in a scan step
+
+__device__ __forceinline__ int pages_of(int len, int page) { return len / page + (len % page != 0); }
+
+// Sum of the threads before this one over one value per thread; *total is the block's sum.  All threads.
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T* total) {
+  __shared__ T part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T y = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const T z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  __syncthreads();                 // the last call's reads of part are done
+  if (lane == 31) part[warp] = y;
+  __syncthreads();
+  if (warp == 0) {
+    T s = part[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const T z = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += z;
+    }
+    part[lane] = s;
+  }
+  __syncthreads();
+  *total = part[31];
+  return y - x + (warp ? part[warp - 1] : 0);
+}
+
+// put(rank, i) for the numbers begin <= i < end with want(i), in order, rank counting from 0.  Returns how many there
+// are, or some number >= enough when it stopped early.  All threads.
+template <typename Want, typename Put>
+__device__ __forceinline__ int ranked(int begin, int end, long long enough, Want want, Put put) {
+  int found = 0;
+  for (long long base = begin; base < end && found < enough; base += kPagesThreads * kPagesPer) {
+    const long long i0 = base + threadIdx.x * kPagesPer;
+    unsigned bits = 0;
+#pragma unroll
+    for (int e = 0; e < kPagesPer; ++e)
+      if (i0 + e < end && want(static_cast<int>(i0) + e)) bits |= 1u << e;
+    int total;
+    int rank = found + block_scan<int>(__popc(bits), &total);
+    for (; bits; bits &= bits - 1) put(rank++, static_cast<int>(i0) + __ffs(bits) - 1);
+    found += total;
+  }
+  return found;
+}
+
+// The pages that n requests want, wants(i) each (0 for a bad request): leaves prefix[i], the pages wanted before
+// request i (at most 2^30, which no cache has), and in list[] the free pages in order, as far as they are wanted.
+// Returns the number of free pages found: request i is granted if prefix[i] + wants(i) is not above it.
+template <typename Wants>
+__device__ __forceinline__ int plan_pages(const PagesArgs& a, Wants wants) {
+  long long need = 0;
+  for (int base = 0; base < a.n; base += kPagesThreads) {
+    const int i = base + threadIdx.x;
+    long long total;
+    const long long before = need + block_scan<long long>(i < a.n ? wants(i) : 0, &total);
+    if (i < a.n) a.prefix[i] = static_cast<int>(before < (1 << 30) ? before : 1 << 30);
+    need += total;
+  }
+  const int found = ranked(0, a.P, need, [&](int i) { return a.refs[i] == 0; },
+                           [&](int rank, int i) { if (rank < need) a.list[rank] = i; });
+  __syncthreads();
+  return found;
+}
+
+// A sequence length that the table can hold.
+__device__ __forceinline__ bool len_ok(const PagesArgs& a, int len) {
+  return len >= 0 && len <= static_cast<long long>(a.M) * a.page;
+}
+
+// Two requests of a call must not change the same sequence: of the requests with snap[i] >= 0 the first that names a
+// sequence keeps it, the others get snap[i] = -1.  snap[] was taken before anything is written.
+template <typename Seq>
+__device__ __forceinline__ void claim_sequences(const PagesArgs& a, Seq seq) {
+  for (int s = threadIdx.x; s < a.S; s += kPagesThreads) a.claim[s] = 0x7fffffff;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += kPagesThreads)
+    if (a.snap[i] >= 0) atomicMin(a.claim + seq(i), i);
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += kPagesThreads)
+    if (a.snap[i] >= 0 && a.claim[seq(i)] != i) a.snap[i] = -1;
+  __syncthreads();
+}
+
+// Sequences grow by tokens and get the pages they need.  snap[i]: the pages wanted, -1 for a bad request.
+__global__ void __launch_bounds__(kPagesThreads) fa_pages_extend_kernel(const PagesArgs a) {
+  for (int i = threadIdx.x; i < a.n; i += kPagesThreads) {
+    const int s = a.seqs[i], t = a.arg[i];
+    int w = -1;
+    if (s >= 0 && s < a.S && t >= 0) {
+      const int len = a.lens[s];
+      if (len_ok(a, len) && static_cast<long long>(len) + t <= static_cast<long long>(a.M) * a.page)
+        w = pages_of(len + t, a.page) - pages_of(len, a.page);
+    }
+    a.snap[i] = w;
+  }
+  claim_sequences(a, [&](int i) { return a.seqs[i]; });
+  const int found = plan_pages(a, [&](int i) { return max(0, a.snap[i]); });
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < a.n; i += kPagesThreads / 32) {      // a warp per request
+    const int w = a.snap[i];
+    const bool ok = w == 0 || (w > 0 && a.prefix[i] + static_cast<long long>(w) <= found);
+    if (ok) {
+      const int s = a.seqs[i], len = a.lens[s];
+      int* row = a.table + s * a.table_stride + pages_of(len, a.page);
+      for (int e = lane; e < w; e += 32) {
+        const int p = a.list[a.prefix[i] + e];
+        row[e] = p;
+        a.refs[p] = 1;
+      }
+      __syncwarp();                                                        // every lane has read the old length
+      if (lane == 0) a.lens[s] = len + a.arg[i];
+    }
+    if (lane == 0) a.status[i] = ok ? 0 : (w < 0 ? 1 : 4);                 // FA_OK, FA_ERR_INVALID, FA_ERR_WORKSPACE
+  }
+}
+
+// Empty sequences become copies of others: whole pages shared, the last page, if not full, to be copied.
+// snap[i]: the source's length, -1 for a bad request.
+__global__ void __launch_bounds__(kPagesThreads) fa_pages_fork_kernel(const PagesArgs a) {
+  for (int i = threadIdx.x; i < a.n; i += kPagesThreads) {
+    const int s = a.seqs[i], t = a.arg[i];
+    int len = -1;
+    if (s >= 0 && s < a.S && t >= 0 && t < a.S && s != t && a.lens[t] == 0 && len_ok(a, a.lens[s])) len = a.lens[s];
+    a.snap[i] = len;
+  }
+  claim_sequences(a, [&](int i) { return a.arg[i]; });
+  auto wants = [&](int i) { return a.snap[i] > 0 && a.snap[i] % a.page != 0 ? 1 : 0; };
+  const int found = plan_pages(a, wants);
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < a.n; i += kPagesThreads / 32) {      // a warp per request
+    const int len = a.snap[i], w = wants(i);
+    const bool ok = len >= 0 && (w == 0 || a.prefix[i] < found);
+    if (ok) {
+      const int full = len / a.page;
+      const int* from = a.table + a.seqs[i] * a.table_stride;
+      int* to = a.table + a.arg[i] * a.table_stride;
+      for (int e = lane; e < full; e += 32) {
+        const int p = from[e];
+        to[e] = p;
+        if (p >= 0 && p < a.P) atomicAdd(a.refs + p, 1);
+        else atomicOr(a.dev_status, DEV_ARGS);
+      }
+      if (lane == 0) {
+        if (w) {
+          const int p = a.list[a.prefix[i]], old = from[full];
+          const bool good = old >= 0 && old < a.P;
+          if (!good) atomicOr(a.dev_status, DEV_ARGS);
+          to[full] = p;
+          a.refs[p] = 1;
+          int* c = a.copies + 3LL * a.prefix[i];      // granted requests come first: the list has no holes
+          c[0] = good ? old : p;
+          c[1] = p;
+          c[2] = good ? len - full * a.page : 0;
+        }
+        a.lens[a.arg[i]] = len;
+      }
+    }
+    if (lane == 0) a.status[i] = ok ? 0 : (len < 0 ? 1 : 4);
+  }
+  // everything behind the granted copies: the list's end
+  __shared__ int copied;
+  if (threadIdx.x == 0) copied = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += kPagesThreads)
+    if (wants(i) && a.prefix[i] < found) atomicMax(&copied, a.prefix[i] + 1);
+  __syncthreads();
+  for (long long e = 3LL * copied + threadIdx.x; e < 3LL * a.n; e += kPagesThreads) a.copies[e] = -1;
+}
+
+// Sequences become empty.  One warp per request; the first to take a sequence's length frees its pages.
+__global__ void __launch_bounds__(128) fa_pages_free_kernel(const PagesArgs a) {
+  const int i = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= a.n) return;
+  const int s = __ldg(a.seqs + i);
+  if (s < 0 || s >= a.S) {
+    if (lane == 0) atomicOr(a.dev_status, DEV_ARGS);
+    return;
+  }
+  int len = 0;
+  if (lane == 0) {
+    len = atomicExch(a.lens + s, 0);
+    if (!len_ok(a, len)) {
+      atomicOr(a.dev_status, DEV_ARGS);
+      len = 0;
+    }
+  }
+  len = __shfl_sync(0xffffffffu, len, 0);
+  int* row = a.table + s * a.table_stride;
+  for (int e = lane; e < pages_of(len, a.page); e += 32) {
+    const int p = row[e];
+    row[e] = -1;
+    if (p < 0 || p >= a.P || atomicSub(a.refs + p, 1) <= 0) {
+      atomicOr(a.dev_status, DEV_ARGS);
+      if (p >= 0 && p < a.P) atomicAdd(a.refs + p, 1);
+    }
+  }
+}
+
+// Ranks the pages in use and the holes among them; lists the moves; moves the reference counts.
+__global__ void __launch_bounds__(kPagesThreads) fa_pages_plan_compact_kernel(const PagesArgs a) {
+  int mine = 0, live;
+  for (int i = threadIdx.x; i < a.P; i += kPagesThreads) mine += a.refs[i] > 0;
+  block_scan<int>(mine, &live);
+  int* hole = a.list;              // holes below `live`: at most live of them, in list[0, live)
+  const int holes = ranked(0, live, 1LL << 62, [&](int i) { return a.refs[i] <= 0; }, [&](int rank, int i) { hole[rank] = i; });
+  __syncthreads();
+  // as many pages in use lie at or above `live`; their new places go to list[i], i >= live
+  for (int i = live + threadIdx.x; i < a.P; i += kPagesThreads) a.list[i] = i;
+  __syncthreads();
+  ranked(live, a.P, 1LL << 62, [&](int i) { return a.refs[i] > 0; },
+         [&](int rank, int i) {
+           const int to = hole[rank];
+           a.list[i] = to;
+           a.refs[to] = a.refs[i];
+           a.refs[i] = 0;
+           int* c = a.copies + 3LL * rank;
+           c[0] = i;
+           c[1] = to;
+           c[2] = a.page;
+         });
+  for (long long e = 3LL * holes + threadIdx.x; e < 3LL * (a.P / 2); e += kPagesThreads) a.copies[e] = -1;
+  if (threadIdx.x == 0) *a.info = live;
+}
+
+// The page tables name the new places.  One warp per sequence.
+__global__ void __launch_bounds__(128) fa_pages_rename_kernel(const PagesArgs a) {
+  const int s = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (s >= a.S) return;
+  const int live = *a.info, len = a.lens[s];
+  if (!len_ok(a, len)) {
+    if (lane == 0) atomicOr(a.dev_status, DEV_ARGS);
+    return;
+  }
+  int* row = a.table + s * a.table_stride;
+  for (int e = lane; e < pages_of(len, a.page); e += 32) {
+    const int p = row[e];
+    if (p < 0 || p >= a.P) atomicOr(a.dev_status, DEV_ARGS);
+    else if (p >= live) row[e] = a.list[p];
+  }
+}
+
+struct PageCopyArgs {
+  __nv_bfloat16 *kp, *vp;
+  Strides sk, sv;                  // {page, head, row}
+  const int* copies;
+  int n, P, page, H_kv, d;
+  uint32_t* status;
+};
+
+// Block x takes rows x, x + grid, ... of the list: its lanes look at 32 of them at once, so a list that is mostly empty
+// costs one read, and its threads copy the listed page's rows, 16 bytes at a time, K then V.
+__global__ void __launch_bounds__(256) fa_pages_copy_kernel(const PageCopyArgs a) {
+  const int vecs = a.d / 8, lane = threadIdx.x & 31;
+  for (long long base = blockIdx.x; base < a.n; base += 32LL * gridDim.x) {
+    const long long mine = base + static_cast<long long>(lane) * gridDim.x;
+    unsigned todo = __ballot_sync(0xffffffffu, mine < a.n && __ldg(a.copies + 3 * mine) >= 0);
+    for (; todo; todo &= todo - 1) {
+      const int* c = a.copies + 3 * (base + static_cast<long long>(__ffs(todo) - 1) * gridDim.x);
+      const int src = __ldg(c), dst = __ldg(c + 1), rows = __ldg(c + 2);
+      if (src >= a.P || dst < 0 || dst >= a.P || rows < 0 || rows > a.page) {
+        if (threadIdx.x == 0) atomicOr(a.status, DEV_ARGS);
+        continue;
+      }
+      const int per = rows * vecs;
+      for (int e = threadIdx.x; e < 2 * a.H_kv * per; e += 256) {
+        const int hk = e / per, r = e - hk * per, row = r / vecs, x = r - row * vecs;
+        const bool k = hk < a.H_kv;
+        __nv_bfloat16* p = k ? a.kp : a.vp;
+        const Strides& st = k ? a.sk : a.sv;
+        const int h = k ? hk : hk - a.H_kv;
+        *reinterpret_cast<uint4*>(p + row_offset(st, dst, h, row) + 8 * x) =
+            *reinterpret_cast<const uint4*>(p + row_offset(st, src, h, row) + 8 * x);
+      }
+    }
+  }
+}
+
+}  // namespace fa

@@ -1,0 +1,342 @@
+// Host side of the serving operators: rotary positions, the paged key/value cache, its attention and its pages.
+// Included behind fa_api.cu, whose device state and checks it uses.
+#pragma once
+
+#include "pages_kernel.cuh"
+#include "paged_decode_kernel.cuh"
+#include "rotary_kernel.cuh"
+
+namespace fa {
+namespace {
+
+bool aligned_to(const void* p, size_t n) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws != nullptr && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
+}
+fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// Strides of an output: rows of different (batch, head, row) do not coincide on an axis.
+bool out_strides_ok(const fa_strides& st, int batch, int heads, int rows) {
+  return (batch <= 1 || st.batch > 0) && (heads <= 1 || st.head > 0) && (rows <= 1 || st.row > 0);
+}
+
+template <typename T, bool APPEND>
+fa_status launch_rotary(const RotArgs& a, int interleaved, cudaStream_t stream) {
+  const long long per = a.r / 2 + a.d - a.r;
+  const long long blocks = (a.tokens * per + 255) / 256;
+  if (blocks >= (1LL << 31)) return FA_ERR_INVALID;
+  fa_rotary_kernel<T, APPEND><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, interleaved);
+  return launched();
+}
+
+// The cache and table of a paged layout.
+fa_status check_paged(const fa_paged_layout& L) {
+  if (L.B < 1 || L.H_kv < 1 || L.num_pages < 1 || L.max_pages < 1 || L.page_size < 1) return FA_ERR_INVALID;
+  if (L.d != 64 && L.d != 128 && L.d != 256) return FA_ERR_UNSUPPORTED;
+  if (L.page_size % 8 != 0 || L.page_size > 65536 || 1LL * L.max_pages * L.page_size >= (1LL << 31) ||
+      L.num_pages >= (1 << 30) || (L.B > 1 && L.table_stride < L.max_pages))
+    return FA_ERR_INVALID;
+  if (!strides_ok(L.k_pages, L.page_size, L.H_kv, L.num_pages) || !strides_ok(L.v_pages, L.page_size, L.H_kv, L.num_pages))
+    return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+fa_status check_decode(const fa_paged_layout& L) {
+  const fa_status st = check_paged(L);
+  if (st != FA_OK) return st;
+  if (L.N < 1 || L.H < 1 || L.H % L.H_kv != 0 || 1LL * L.B * L.H * L.N >= (1LL << 31)) return FA_ERR_INVALID;
+  if (!strides_ok(L.q, L.N, L.H, L.B) || !strides_ok(L.o, L.N, L.H, L.B)) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+bool pages_layout_ok(const fa_pages_layout* L) {
+  return L != nullptr && L->num_seqs >= 1 && L->num_pages >= 1 && L->num_pages < (1 << 30) && L->page_size >= 1 &&
+         L->max_pages >= 1 && 1LL * L->max_pages * L->page_size < (1LL << 31) &&
+         (L->num_seqs == 1 || L->table_stride >= L->max_pages);
+}
+
+// Workspace of the page calls: claim [S], snap [n], prefix [n], list [P], info [1].
+size_t pages_ws_bytes(const fa_pages_layout& L, int n) {
+  return round256(4 * static_cast<size_t>(L.num_seqs)) + 2 * round256(4 * static_cast<size_t>(n)) +
+         round256(4 * static_cast<size_t>(L.num_pages)) + 256;
+}
+
+fa_status pages_args(PagesArgs* a, int32_t* table, int32_t* lens, int32_t* refs, const fa_pages_layout* L, int n,
+                     void* ws, size_t ws_bytes, bool need_ws) {
+  if (!pages_layout_ok(L) || n < 0) return FA_ERR_INVALID;
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4)) return FA_ERR_ALIGN;
+  if (need_ws && !workspace_ok(ws, ws_bytes, pages_ws_bytes(*L, n))) return FA_ERR_WORKSPACE;
+  DevState* ds = nullptr;
+  const fa_status st = device_state(&ds);
+  if (st != FA_OK) return st;
+  *a = PagesArgs();
+  a->table = table;
+  a->table_stride = L->table_stride;
+  a->lens = lens;
+  a->refs = refs;
+  a->S = L->num_seqs;
+  a->P = L->num_pages;
+  a->page = L->page_size;
+  a->M = L->max_pages;
+  a->n = n;
+  if (need_ws) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    a->claim = reinterpret_cast<int*>(w);
+    w += round256(4 * static_cast<size_t>(L->num_seqs));
+    a->snap = reinterpret_cast<int*>(w);
+    w += round256(4 * static_cast<size_t>(n));
+    a->prefix = reinterpret_cast<int*>(w);
+    w += round256(4 * static_cast<size_t>(n));
+    a->list = reinterpret_cast<int*>(w);
+    w += round256(4 * static_cast<size_t>(L->num_pages));
+    a->info = reinterpret_cast<int*>(w);
+  }
+  a->dev_status = ds->status;
+  return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                    const double* freqs, const fa_rotary_layout* layout, float magnitude, int inverse,
+                    fa_dtype dtype, fa_stream_t stream) {
+  if (layout == nullptr) return FA_ERR_INVALID;
+  const fa_rotary_layout& L = *layout;
+  if (L.B < 1 || L.H < 1 || L.H_kv < 0 || L.N < 0 || L.d < 1 || L.d > 1024 || L.rotary_dim < 0 || L.rotary_dim > L.d ||
+      L.rotary_dim % 2 != 0 || 1LL * L.B * L.N >= (1LL << 31) || !std::isfinite(magnitude) ||
+      !out_strides_ok(L.q_out, L.B, L.H, L.N) || (L.H_kv > 0 && !out_strides_ok(L.k_out, L.B, L.H_kv, L.N)))
+    return FA_ERR_INVALID;
+  if (dtype != FA_BF16 && dtype != FA_F32) return FA_ERR_UNSUPPORTED;
+  if (L.N == 0) return FA_OK;   // no row (and perhaps no memory)
+  const size_t es = dtype == FA_F32 ? 4 : 2;
+  if (!aligned_to(q, es) || !aligned_to(q_out, es) || (L.H_kv > 0 && (!aligned_to(k, es) || !aligned_to(k_out, es))) ||
+      (positions != nullptr && !aligned_to(positions, 4)) || (L.rotary_dim > 0 && !aligned_to(freqs, 8)))
+    return FA_ERR_ALIGN;
+  RotArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.qo = q_out;
+  a.ko = k_out;
+  a.sq = kstrides(L.q);
+  a.sk = kstrides(L.k);
+  a.sqo = kstrides(L.q_out);
+  a.sko = kstrides(L.k_out);
+  a.pos = positions;
+  a.pos_b = L.positions_batch;
+  a.freqs = freqs;
+  a.B = L.B;
+  a.N = L.N;
+  a.H = L.H;
+  a.H_kv = L.H_kv;
+  a.d = L.d;
+  a.r = L.rotary_dim;
+  a.tokens = 1LL * L.B * L.N;
+  a.magnitude = magnitude;
+  a.inverse = inverse;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == FA_F32 ? launch_rotary<float, false>(a, L.interleaved, s)
+                         : launch_rotary<__nv_bfloat16, false>(a, L.interleaved, s);
+}
+
+fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, void* k_pages, void* v_pages,
+                          const int32_t* page_table, const int32_t* seq_lens, const double* freqs,
+                          const fa_paged_layout* layout, float magnitude, fa_stream_t stream) {
+  if (layout == nullptr) return FA_ERR_INVALID;
+  const fa_paged_layout& L = *layout;
+  fa_status st = check_paged(L);
+  if (st != FA_OK) return st;
+  const bool pk = L.cu_seqlens != nullptr;
+  const long long tokens = pk ? L.total : 1LL * L.B * L.N;
+  if ((pk ? L.total : L.N) < 0 || tokens >= (1LL << 31) || (q != nullptr && L.H < 1) || !std::isfinite(magnitude) ||
+      (freqs != nullptr && (L.rotary_dim < 0 || L.rotary_dim > L.d || L.rotary_dim % 2 != 0)))
+    return FA_ERR_INVALID;
+  if (tokens == 0) return FA_OK;
+  const int nb = pk ? 1 : L.B, rows = pk ? L.total : L.N;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned_to(page_table, 4) ||
+      !aligned_to(seq_lens, 4) || (pk && !aligned_to(L.cu_seqlens, 4)) || (freqs != nullptr && !aligned_to(freqs, 8)) ||
+      (q != nullptr && (!aligned16(q) || !aligned16(o))) || !strides_ok(L.k, rows, L.H_kv, nb) ||
+      !strides_ok(L.v, rows, L.H_kv, nb) ||
+      (q != nullptr && (!strides_ok(L.q, rows, L.H, nb) || !strides_ok(L.o, rows, L.H, nb))))
+    return FA_ERR_ALIGN;
+  DevState* ds = nullptr;
+  if ((st = device_state(&ds)) != FA_OK) return st;
+  RotArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qo = o;
+  a.ko = k_pages;
+  a.vo = v_pages;
+  a.sq = kstrides(L.q);
+  a.sk = kstrides(L.k);
+  a.sv = kstrides(L.v);
+  a.sqo = kstrides(L.o);
+  a.sko = kstrides(L.k_pages);
+  a.svo = kstrides(L.v_pages);
+  a.freqs = freqs;
+  a.B = L.B;
+  a.N = L.N;
+  a.H = q != nullptr ? L.H : 0;
+  a.H_kv = L.H_kv;
+  a.d = L.d;
+  a.r = freqs != nullptr ? L.rotary_dim : 0;
+  a.tokens = tokens;
+  a.magnitude = magnitude;
+  a.table = page_table;
+  a.table_stride = L.table_stride;
+  a.seq_lens = seq_lens;
+  a.cu = L.cu_seqlens;
+  a.total = L.total;
+  a.num_pages = L.num_pages;
+  a.page = L.page_size;
+  a.max_pages = L.max_pages;
+  a.status = ds->status;
+  return launch_rotary<__nv_bfloat16, true>(a, L.interleaved, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_paged_decode_workspace_size(const fa_paged_layout* layout) {
+  if (layout == nullptr || check_decode(*layout) != FA_OK) return 0;
+  return 256;
+}
+
+fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                          const int32_t* seq_lens, void* o, float* lse, const fa_paged_layout* layout, float scale,
+                          int causal, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  if (layout == nullptr) return FA_ERR_INVALID;
+  const fa_paged_layout& L = *layout;
+  fa_status st = check_decode(L);
+  if (st != FA_OK) return st;
+  if (!scale_ok(scale)) return FA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned_to(lse, 4) ||
+      !aligned_to(page_table, 4) || !aligned_to(seq_lens, 4))
+    return FA_ERR_ALIGN;
+  if (!workspace_ok(workspace, workspace_bytes, fa_paged_decode_workspace_size(layout))) return FA_ERR_WORKSPACE;
+  DevState* ds = nullptr;
+  if ((st = device_state(&ds)) != FA_OK) return st;
+  PagedArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kp = static_cast<const __nv_bfloat16*>(k_pages);
+  a.vp = static_cast<const __nv_bfloat16*>(v_pages);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.table = page_table;
+  a.table_stride = L.table_stride;
+  a.seq_lens = seq_lens;
+  a.sq = kstrides(L.q);
+  a.so = kstrides(L.o);
+  a.skp = kstrides(L.k_pages);
+  a.svp = kstrides(L.v_pages);
+  a.B = L.B;
+  a.H = L.H;
+  a.H_kv = L.H_kv;
+  a.N = L.N;
+  a.group = L.H / L.H_kv;
+  a.num_pages = L.num_pages;
+  a.page = L.page_size;
+  a.max_pages = L.max_pages;
+  a.causal = causal ? 1 : 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.status = ds->status;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const unsigned blocks = static_cast<unsigned>((1LL * L.B * L.H * L.N + 3) / 4);
+  if (L.d == 64) fa_paged_decode_kernel<64><<<blocks, 128, 0, s>>>(a);
+  else if (L.d == 128) fa_paged_decode_kernel<128><<<blocks, 128, 0, s>>>(a);
+  else fa_paged_decode_kernel<256><<<blocks, 128, 0, s>>>(a);
+  return launched();
+}
+
+size_t fa_pages_workspace_size(const fa_pages_layout* layout, int n) {
+  return pages_layout_ok(layout) && n >= 0 ? pages_ws_bytes(*layout, n) : 0;
+}
+
+fa_status fa_pages_extend(int32_t* page_table, int32_t* seq_lens, int32_t* refcounts, const fa_pages_layout* layout,
+                          const int32_t* seqs, const int32_t* tokens, int n, int32_t* status, void* workspace,
+                          size_t workspace_bytes, fa_stream_t stream) {
+  PagesArgs a;
+  if (n > 0 && (!aligned_to(seqs, 4) || !aligned_to(tokens, 4) || !aligned_to(status, 4))) return FA_ERR_ALIGN;
+  const fa_status st = pages_args(&a, page_table, seq_lens, refcounts, layout, n, workspace, workspace_bytes, true);
+  if (st != FA_OK || n == 0) return st;
+  a.seqs = seqs;
+  a.arg = tokens;
+  a.status = status;
+  fa_pages_extend_kernel<<<1, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+fa_status fa_pages_fork(int32_t* page_table, int32_t* seq_lens, int32_t* refcounts, const fa_pages_layout* layout,
+                        const int32_t* src, const int32_t* dst, int n, int32_t* copies, int32_t* status,
+                        void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  PagesArgs a;
+  if (n > 0 && (!aligned_to(src, 4) || !aligned_to(dst, 4) || !aligned_to(copies, 4) || !aligned_to(status, 4)))
+    return FA_ERR_ALIGN;
+  const fa_status st = pages_args(&a, page_table, seq_lens, refcounts, layout, n, workspace, workspace_bytes, true);
+  if (st != FA_OK || n == 0) return st;
+  a.seqs = src;
+  a.arg = dst;
+  a.copies = copies;
+  a.status = status;
+  fa_pages_fork_kernel<<<1, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+fa_status fa_pages_free(int32_t* page_table, int32_t* seq_lens, int32_t* refcounts, const fa_pages_layout* layout,
+                        const int32_t* seqs, int n, fa_stream_t stream) {
+  PagesArgs a;
+  if (n > 0 && !aligned_to(seqs, 4)) return FA_ERR_ALIGN;
+  const fa_status st = pages_args(&a, page_table, seq_lens, refcounts, layout, n, nullptr, 0, false);
+  if (st != FA_OK || n == 0) return st;
+  a.seqs = seqs;
+  fa_pages_free_kernel<<<(n + 3) / 4, 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+fa_status fa_pages_compact(int32_t* page_table, const int32_t* seq_lens, int32_t* refcounts,
+                           const fa_pages_layout* layout, int32_t* copies, void* workspace, size_t workspace_bytes,
+                           fa_stream_t stream) {
+  PagesArgs a;
+  if (layout != nullptr && layout->num_pages > 1 && !aligned_to(copies, 4)) return FA_ERR_ALIGN;
+  const fa_status st = pages_args(&a, page_table, const_cast<int32_t*>(seq_lens), refcounts, layout, 0, workspace,
+                                  workspace_bytes, true);
+  if (st != FA_OK) return st;
+  a.copies = copies;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  fa_pages_plan_compact_kernel<<<1, kPagesThreads, 0, s>>>(a);
+  fa_pages_rename_kernel<<<(a.S + 3) / 4, 128, 0, s>>>(a);
+  return launched();
+}
+
+fa_status fa_pages_copy(void* k_pages, void* v_pages, const int32_t* copies, int n, const fa_paged_layout* layout,
+                        fa_stream_t stream) {
+  if (layout == nullptr) return FA_ERR_INVALID;
+  const fa_paged_layout& L = *layout;
+  if (n < 0 || L.H_kv < 1 || L.num_pages < 1 || L.page_size < 1 || L.d < 8 || L.d % 8 != 0 ||
+      2LL * L.H_kv * L.page_size * L.d >= (1LL << 31))
+    return FA_ERR_INVALID;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || (n > 0 && !aligned_to(copies, 4)) ||
+      !strides_ok(L.k_pages, L.page_size, L.H_kv, L.num_pages) || !strides_ok(L.v_pages, L.page_size, L.H_kv, L.num_pages))
+    return FA_ERR_ALIGN;
+  if (n == 0) return FA_OK;
+  DevState* ds = nullptr;
+  const fa_status st = device_state(&ds);
+  if (st != FA_OK) return st;
+  PageCopyArgs a;
+  a.kp = static_cast<__nv_bfloat16*>(k_pages);
+  a.vp = static_cast<__nv_bfloat16*>(v_pages);
+  a.sk = kstrides(L.k_pages);
+  a.sv = kstrides(L.v_pages);
+  a.copies = copies;
+  a.n = n;
+  a.P = L.num_pages;
+  a.page = L.page_size;
+  a.H_kv = L.H_kv;
+  a.d = L.d;
+  a.status = ds->status;
+  const int grid = n < ds->sms * 8 ? n : ds->sms * 8;
+  fa_pages_copy_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+}  // extern "C"

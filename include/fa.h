@@ -243,6 +243,156 @@ fa_status fa_decode(const void* q, const void* k, const void* v, void* o, float*
 size_t fa_decode_workspace_size(int B, int H, int H_kv, int Lq, int Nk, int d);
 
 /*
+ * Rotary positions.  Row `pos` of a head is turned pair by pair of its first
+ * rotary_dim columns, pair i by the angle pos * freqs[i]:
+ *     y_a = magnitude (x_a cos - x_b sin),  y_b = magnitude (x_b cos + x_a sin),
+ * pair i being columns (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when
+ * interleaved != 0; the other columns are copied.  inverse != 0 turns by the
+ * negative angle (magnitude unchanged): the transpose of the map, hence its
+ * backward pass (pass the gradients of q_out, k_out as q, k).
+ *  q, q_out: [batch][H][row][d];  k, k_out: [batch][H_kv][row][d] (H_kv = 0:
+ *  no k, the pointers may be null), element type dtype, d contiguous, any
+ *  strides (0 included) on the inputs; the strides of the outputs positive
+ *  where the extent is above 1.  An output may be its input (same strides).
+ *  positions: DEVICE int32, row n of batch entry b at positions[b *
+ *  positions_batch + n]; NULL: row n has position n.  freqs: DEVICE double
+ *  [rotary_dim / 2], radians per position, finite.  Angles are formed in fixed
+ *  point as fractions of a turn, exact for every int32 position; products and
+ *  sums are 32-bit, one rounding to dtype at the end.
+ * rotary_dim even, 0 <= rotary_dim <= d <= 1024 (FA_ERR_INVALID; d need not be
+ * a multiple of 8).  B, H >= 1, N >= 0; B * N < 2^31.  Pointers are aligned to the element size
+ * (FA_ERR_ALIGN); 16-byte aligned pointers and strides take the vector path.
+ */
+typedef struct {
+  int B, H, H_kv, N, d;
+  int rotary_dim, interleaved;
+  int64_t positions_batch;      /* elements between batch entries' positions (0: shared) */
+  fa_strides q, k, q_out, k_out;
+} fa_rotary_layout;
+
+fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                    const double* freqs, const fa_rotary_layout* layout, float magnitude, int inverse,
+                    fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * Paged key/value cache.  k_pages and v_pages are [num_pages][H_kv][page_size][d]
+ * bf16 with any page / head / row strides (fa_strides.batch is the page stride;
+ * positive multiples of 8 elements, d contiguous).  Sequence b holds keys
+ * 0 .. seq_lens[b] - 1; key j is row j % page_size of page
+ * page_table[b * table_stride + j / page_size].  page_table and seq_lens are
+ * DEVICE int32; the entries of a row behind its last page are never used.
+ * d in {64, 128, 256} (FA_ERR_UNSUPPORTED); page_size a multiple of 8, at most
+ * 65536, and max_pages (entries of a table row) >= 1 with max_pages * page_size < 2^31
+ * (FA_ERR_INVALID).  A sequence length that is negative or beyond max_pages *
+ * page_size, and a page number outside 0 .. num_pages - 1, are reported by
+ * fa_get_device_status as FA_ERR_INVALID; no memory outside the tensors is
+ * touched, and that sequence's results are undefined.
+ */
+typedef struct {
+  int B, H, H_kv, d;
+  int N;                        /* query rows / new tokens per sequence (packed: ignored)      */
+  int num_pages, page_size, max_pages;
+  int64_t table_stride;         /* elements between rows of page_table                         */
+  fa_strides q, o;              /* strides of q and its output                                  */
+  fa_strides k, v;              /* strides of the new keys and values (fa_paged_append)         */
+  fa_strides k_pages, v_pages;  /* {page, head, row} strides of the cache                       */
+  const int32_t* cu_seqlens;    /* fa_paged_append, packed: DEVICE B + 1 row offsets; else NULL */
+  int total;                    /* packed: rows of q, k, v                                      */
+  int rotary_dim, interleaved;  /* fa_paged_append with freqs                                   */
+} fa_paged_layout;
+
+/*
+ * Writes new keys and values into the pages: token i of the n of sequence b
+ * goes to position seq_lens[b] - n + i, so seq_lens holds the lengths AFTER the
+ * call (and is what fa_paged_decode takes next).  n = N for every sequence
+ * (k, v: [batch][H_kv][row][d]), or packed rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] (k, v: [row][H_kv][d], batch strides unused).
+ * freqs != NULL: the keys are first turned by fa_rotary's map at their
+ * positions.  q != NULL: the queries ([.][H][.][d]) are turned the same way into
+ * o, which may be q (same strides).  A token whose position is negative (a
+ * sequence shorter than n: padding) is not written and its row of o is zero.
+ * A packed row outside every sequence is not written either; its row of o is
+ * zero, or what it was when o is q.  Two sequences must not receive tokens
+ * on the same page.  H is only used with q.
+ */
+fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, void* k_pages, void* v_pages,
+                          const int32_t* page_table, const int32_t* seq_lens, const double* freqs,
+                          const fa_paged_layout* layout, float magnitude, fa_stream_t stream);
+
+/*
+ * Attention of each sequence's last N positions over its pages: q, o:
+ * [batch][H][row][d] bf16 (positive strides that are multiples of 8 elements),
+ * lse: dense [B, H, N] float.
+ * causal != 0: query i sees keys j <= seq_lens[b] - N + i.  Otherwise the
+ * definition of fa_decode; a query that sees no key (an empty sequence, or N >
+ * seq_lens[b]) gets o = 0, lse = -inf.  H a multiple of H_kv; N >= 1.  What
+ * the pages hold behind a sequence's end does not matter (NaN included); a key
+ * that only some of the N queries see has to be finite.
+ * workspace: at least fa_paged_decode_workspace_size(layout) bytes, 256-byte
+ * aligned; not shared by calls that may overlap.
+ */
+fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                          const int32_t* seq_lens, void* o, float* lse, const fa_paged_layout* layout,
+                          float scale, int causal, void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Bytes of workspace fa_paged_decode needs (0 for a layout it rejects). */
+size_t fa_paged_decode_workspace_size(const fa_paged_layout* layout);
+
+/*
+ * Bookkeeping of pages, on the device and without a copy to the host.  The state of a cache is
+ *   page_table [num_seqs][max_pages] (rows table_stride apart), seq_lens [num_seqs], refcounts [num_pages],
+ * all DEVICE int32: sequence s owns the first ceil(seq_lens[s] / page_size) entries of its row, refcounts
+ * counts the rows that hold a page, and a page is free when that is 0.  New pages are the free pages of
+ * lowest number, handed out in the order of the requests, so results do not depend on timing.  A page that is
+ * not full belongs to one sequence only.  Calls on one state have to be ordered (one stream).  workspace:
+ * fa_pages_workspace_size(layout, n) bytes, 256-byte aligned.
+ * 1 <= num_seqs, num_pages, max_pages; page_size >= 1; max_pages * page_size < 2^31; n >= 0
+ * (n = 0 launches nothing).
+ *
+ * fa_pages_extend: sequence seqs[i] grows by tokens[i] >= 0 positions and gets the pages they need.
+ * fa_pages_fork:   the empty sequence dst[i] becomes a copy of src[i] as it was before the call: whole
+ *   pages are shared, a last page that is not full is replaced by a new page.  copies [n][3] lists the
+ *   (source page, new page, rows in use) that fa_pages_copy has to copy, a -1 row behind the last.
+ * fa_pages_free:   sequences seqs[i] become empty; pages nobody holds any more are free (twice the same
+ *   sequence is the same as once).
+ * fa_pages_compact: the pages in use move to numbers below their count: the j-th page in use at or above the
+ *   count goes to the j-th free number below it.  copies [num_pages / 2][3] lists the moves, -1 behind
+ *   the last; page_table and refcounts name the new places.
+ * status[i] (extend, fork): 0 done; FA_ERR_WORKSPACE: no page left (a request is granted when the pages that it and all
+ *   valid requests before it need were free); FA_ERR_INVALID: a sequence number out of range or asked for twice in one call, a
+ *   negative length or count, more than max_pages pages, dst not empty.  A request that is not granted changes nothing.
+ * Table entries outside 0 .. num_pages - 1 in a part that is in use, and bad numbers in fa_pages_free, are skipped and
+ * reported by fa_get_device_status as FA_ERR_INVALID.
+ */
+typedef struct {
+  int num_seqs, num_pages, page_size, max_pages;
+  int64_t table_stride;
+} fa_pages_layout;
+
+size_t fa_pages_workspace_size(const fa_pages_layout* layout, int n);
+fa_status fa_pages_extend(int32_t* page_table, int32_t* seq_lens, int32_t* refcounts, const fa_pages_layout* layout,
+                          const int32_t* seqs, const int32_t* tokens, int n, int32_t* status,
+                          void* workspace, size_t workspace_bytes, fa_stream_t stream);
+fa_status fa_pages_fork(int32_t* page_table, int32_t* seq_lens, int32_t* refcounts, const fa_pages_layout* layout,
+                        const int32_t* src, const int32_t* dst, int n, int32_t* copies, int32_t* status,
+                        void* workspace, size_t workspace_bytes, fa_stream_t stream);
+fa_status fa_pages_free(int32_t* page_table, int32_t* seq_lens, int32_t* refcounts, const fa_pages_layout* layout,
+                        const int32_t* seqs, int n, fa_stream_t stream);
+fa_status fa_pages_compact(int32_t* page_table, const int32_t* seq_lens, int32_t* refcounts,
+                           const fa_pages_layout* layout, int32_t* copies, void* workspace, size_t workspace_bytes,
+                           fa_stream_t stream);
+
+/*
+ * Copies the first copies[i][2] rows of every head of page copies[i][0] to page copies[i][1], in k_pages and
+ * in v_pages; rows i with a negative source are skipped.  The pages written have to be distinct and none of them
+ * read (rows with page numbers or row counts out of range are skipped and reported by fa_get_device_status as
+ * FA_ERR_INVALID).  Reads B, H_kv, d, num_pages, page_size, k_pages, v_pages of
+ * `layout` only (d a multiple of 8); one call per layer's cache.
+ */
+fa_status fa_pages_copy(void* k_pages, void* v_pages, const int32_t* copies, int n, const fa_paged_layout* layout,
+                        fa_stream_t stream);
+
+/*
  * Backward without a caller-supplied workspace.  Same arguments, outputs and
  * numerics as fa_bwd, minus the workspace pair.  The pages have no counterpart
  * of this call; it exists for callers that cannot allocate device memory

@@ -1,0 +1,164 @@
+"""Rotary positions on the GPU against the float64 oracle.
+
+Bound per element: half a step of the output type, |ref| 2^-8 (bf16) or |ref| 2^-24 (fp32), and what 32-bit arithmetic
+before that rounding can add: the angle is rounded to 2^-24 of half a turn (pi 2^-24 = 1.9e-7), sin and cos to two
+steps (2.4e-7), two products and a sum to half a step each (1.8e-7), all of them times m (|x_a| + |x_b|): under 1e-6 of
+that.  The frequency itself, a double divided by 2 pi, is good to 2^-52 relative, so position p adds |p f| 2^-52 2 pi.
+"""
+import numpy as np
+import pytest
+
+from exact_io_aware_100_b200 import inputs
+from helpers import to_device, to_f64
+from oracle import serving as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _data(seed, shape, dtype, name="q"):
+    host = inputs.make_tensor(seed, name, shape, dtype=dtype)
+    return to_device(host, dtype), inputs.to_f64(host, dtype)
+
+
+def _check(got, x, pos, freqs, m, interleaved, inverse, dtype):
+    want = ref.rotary(x, pos, freqs, m, interleaved, inverse)
+    r = 2 * len(freqs)
+    size = np.zeros_like(want)
+    a, b = (x[..., 0:r:2], x[..., 1:r:2]) if interleaved else (x[..., :r // 2], x[..., r // 2:r])
+    both = m * (np.abs(a) + np.abs(b))
+    far = np.abs(np.broadcast_to(np.asarray(pos, float), (x.shape[0], x.shape[2])))[:, None, :, None] * np.asarray(freqs)
+    add = both * (1e-6 + 2 * np.pi * 2.0 ** -52 * far)
+    if interleaved:
+        size[..., 0:r:2] = size[..., 1:r:2] = add
+    else:
+        size[..., :r // 2] = size[..., r // 2:r] = add
+    bound = size + np.abs(want) * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24)
+    g = to_f64(got)
+    assert np.isfinite(g).all()
+    assert (np.abs(g - want) <= bound).all(), float((np.abs(g - want) - bound).max())
+    assert np.array_equal(g[..., r:], x[..., r:])               # what is not turned is copied
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,H_kv,N,d,r,interleaved,first", [
+    (1, 1, 1, 1, 64, 64, False, 0),           # one row, position 0
+    (2, 4, 2, 37, 64, 64, True, 5),
+    (2, 8, 2, 130, 128, 128, False, 1000),
+    (1, 3, 1, 17, 128, 40, True, 7),          # a part of the head: whole vectors
+    (1, 3, 3, 17, 128, 40, False, 7),         # half pairs of 20 columns: no whole vectors
+    (1, 2, 1, 9, 96, 32, False, 3),
+    (2, 2, 1, 5, 30, 10, True, 3),            # d not a multiple of 8
+    (2, 2, 1, 5, 31, 10, False, 3),           # odd d: rows start at odd elements
+    (1, 5, 1, 3, 256, 0, False, 0),           # nothing to turn: a copy
+    (1, 2, 2, 3, 256, 256, False, 2**31 - 4), # the furthest positions
+    (1, 2, 2, 3, 64, 64, True, -3),           # positions before the start
+    (3, 1, 0, 8, 1024, 512, True, 10**6),     # no k, the widest head
+    (1, 40, 8, 300, 128, 128, False, 0),
+])
+def test_rotary_matches_oracle(B, H, H_kv, N, d, r, interleaved, first, dtype):
+    import torch
+    import exact_io_aware_100_b200 as fa
+    q, fq = _data(700 + N, (B, H, N, d), dtype)
+    k, fk = _data(700 + N, (B, H_kv, N, d), dtype, "k") if H_kv else (None, None)
+    freqs, _ = fa.rotary_frequencies(r)
+    pos = torch.arange(first, first + N, dtype=torch.int64).to(torch.int32).cuda()
+    hf, hp = freqs.cpu().numpy(), pos.cpu().numpy()
+    yq, yk = fa.rotary(q, k, freqs, pos, interleaved, 1.25)
+    gq, gk = fa.rotary_backward(q, k, freqs, pos, interleaved, 1.25)
+    assert (yk is None) == (k is None)
+    _check(yq, fq, hp, hf, 1.25, interleaved, False, dtype)
+    _check(gq, fq, hp, hf, 1.25, interleaved, True, dtype)
+    if H_kv:
+        _check(yk, fk, hp, hf, 1.25, interleaved, False, dtype)
+        _check(gk, fk, hp, hf, 1.25, interleaved, True, dtype)
+    assert fa.fa_get_device_status() == fa.FA_OK
+
+
+def test_rotary_positions_per_batch_entry_and_default():
+    import torch
+    import exact_io_aware_100_b200 as fa
+    q, fq = _data(801, (3, 2, 11, 64), "bf16")
+    freqs, m = fa.rotary_frequencies(32, 500.0, "yarn", 8.0, 64)
+    pos = torch.randint(-50, 5000, (3, 22), dtype=torch.int32, device="cuda")[:, ::1][:, 4:15]     # a strided view
+    y, _ = fa.rotary(q, None, freqs, pos, magnitude=m)
+    _check(y, fq, pos.cpu().numpy(), freqs.cpu().numpy(), m, False, False, "bf16")
+    y, _ = fa.rotary(q, None, freqs)
+    _check(y, fq, np.arange(11), freqs.cpu().numpy(), 1.0, False, False, "bf16")
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_layouts_give_the_same_bits(interleaved):
+    """Token-major, sliced, misaligned, expanded and packed inputs, other output strides, and in place."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    freqs, _ = fa.rotary_frequencies(64)
+    base = torch.randn(2, 21, 6, 64, device="cuda").bfloat16()
+    x = base.transpose(1, 2)                                            # [B, H, N, d] of token-major memory
+    want, want_k = fa.rotary(x.contiguous(), x[:, :2].contiguous(), freqs, interleaved=interleaved)
+    got, got_k = fa.rotary(x, x[:, :2], freqs, interleaved=interleaved)
+    assert got.stride() == x.stride() and torch.equal(got, want) and torch.equal(got_k, want_k)
+    odd = torch.empty(2 * 6 * 21 * 67 + 1, device="cuda", dtype=torch.bfloat16)[1:].view(2, 6, 21, 67)[..., 2:66]
+    odd.copy_(x)                                                        # rows of 67 elements, not even 4-byte aligned
+    out = torch.full_like(odd, 7.0)
+    fa.rotary(odd, None, freqs, interleaved=interleaved, out=(out, None))
+    assert torch.equal(out, want)
+    one = x[:1, :1].expand(2, 6, 21, 64)                                 # broadcast over batch and heads: strides 0
+    got, _ = fa.rotary(one, None, freqs, interleaved=interleaved)
+    assert torch.equal(got, want[:1, :1].expand_as(got))
+    packed = base.reshape(42, 6, 64)
+    pos = torch.arange(21, dtype=torch.int32, device="cuda").repeat(2)
+    got, _ = fa.rotary(packed, None, freqs, pos, interleaved)
+    assert torch.equal(got.view(2, 21, 6, 64).transpose(1, 2), want)
+    there = x.clone()
+    res, _ = fa.rotary(there, None, freqs, interleaved=interleaved, out=(there, None))
+    assert res is there and torch.equal(there, want)
+
+
+def test_rotary_empty_and_large_batches():
+    import torch
+    import exact_io_aware_100_b200 as fa
+    freqs, _ = fa.rotary_frequencies(64)
+    y, _ = fa.rotary(torch.empty(2, 3, 0, 64, device="cuda", dtype=torch.bfloat16), None, freqs)
+    assert y.shape == (2, 3, 0, 64)
+    x = torch.randn(1, 1, 70001, 64, device="cuda").bfloat16()
+    y, _ = fa.rotary(x, None, freqs)
+    f = freqs.cpu().numpy()
+    for i in (0, 4095, 65536, 70000):
+        _check(y[:, :, i:i + 1], to_f64(x[:, :, i:i + 1]), [i], f, 1.0, False, False, "bf16")
+
+
+def test_rotary_offsets_beyond_32_bits():
+    """Rows more than 2^31 elements apart."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    freqs, _ = fa.rotary_frequencies(64)
+    store = torch.empty((1 << 31) + 4096, device="cuda", dtype=torch.bfloat16)
+    x = torch.as_strided(store, (2, 2, 3, 64), ((1 << 31) + 512, 256, 64, 1))
+    x.copy_(torch.randn(2, 2, 3, 64, device="cuda"))
+    want, _ = fa.rotary(x.contiguous(), None, freqs)
+    fa.rotary(x, None, freqs, out=(x, None))
+    assert torch.equal(x, want)
+
+
+def test_rotary_stream_and_graph():
+    import torch
+    import exact_io_aware_100_b200 as fa
+    freqs, _ = fa.rotary_frequencies(128)
+    q, k = torch.randn(2, 4, 33, 128, device="cuda").bfloat16(), torch.randn(2, 2, 33, 128, device="cuda").bfloat16()
+    want = fa.rotary(q, k, freqs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = fa.rotary(q, k, freqs, stream=side)
+    raw = fa.rotary(q, k, freqs, stream=side.cuda_stream)
+    side.synchronize()
+    for g in (got, raw):
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fa.rotary(q, k, freqs)
+        back = fa.rotary_backward(*out, freqs)
+    q.copy_(torch.randn_like(q))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], fa.rotary(q, None, freqs)[0])
+    assert (back[0].float() - q.float()).abs().max() < 0.06       # a turn there and back: two roundings of |x| < 6
