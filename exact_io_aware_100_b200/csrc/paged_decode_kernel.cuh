@@ -1,6 +1,29 @@
 // Attention of the last N positions of each sequence over a paged key/value
 // cache: o = softmax(scale q K^T) V over keys j < seq_len (and j <= seq_len - N + i
 // when causal), lse = ln sum exp.
+//
+// Each key and value is needed once per key/value head by group * N query rows:
+// 4 d bytes and 4 d group N flops per key, so a few rows are bound by HBM.  What
+// carries the kernel is therefore bytes in flight and an even share for every SM:
+//
+//  * the keys of all (sequence, key/value head) pairs, in tiles of KT keys, are one
+//    line of work that is cut into equal ranges, one per warp (kPagedWorkers of them,
+//    all resident at once), whatever the lengths are.  A range covers the end of one
+//    pair, whole pairs, and the beginning of another; whole pairs are written out,
+//    the cut ones leave (max, sum, O) partials that the merge kernel joins.  The
+//    lengths are read on the device: a captured call follows them;
+//  * a warp fills its own ring of tiles with 16-byte asynchronous copies, across the
+//    ends of pairs, and waits for nobody: no block barrier in the loop.  A tile is
+//    gathered 8 keys at a time (8 divides the page size), and the page numbers of 256
+//    keys are read ahead.  Keys behind the sequence's end are filled with zeros in
+//    shared memory, so what the pages hold there does not matter;
+//  * the products are warp-level matrix instructions (16 rows x 8 columns x 16): rows
+//    are few, and the tcgen05 tiles start at 64 rows.  S = Q K^T gives its accumulators
+//    in the layout that P V wants its left operand in, so P stays in registers;
+//  * P is split in two bf16 parts, hi + lo (16 bits of mantissa): with at most 8 rows
+//    the lo parts ride in the 8 unused rows of the same instruction, otherwise they
+//    take a second one.  Everything else is 32-bit; O is rounded once.
+//  * O is rescaled only when a row's maximum grows by more than 2^8.
 #pragma once
 
 #include "layout.cuh"
@@ -16,9 +39,16 @@ struct PagedArgs {
   const int* seq_lens;
   Strides sq, so, skp, svp;        // skp, svp: {page, head, row}
   int B, H, H_kv, N, group;
+  int rows;                        // group * N
   int num_pages, page, max_pages;
   int causal;
   float scale_log2;
+  int workers;                     // warps that share the work of one row tile
+  int row_tiles;
+  int part_rows;                   // rows of a partial
+  float* part_o;                   // [row tile][worker][2][part_rows][D]
+  float2* part_ml;                 // [row tile][worker][2][part_rows] maximum (log2 units) and sum
+  int2* meta;                      // [row tile][B][H_kv] worker where the pair begins, workers it goes on into
   uint32_t* status;
 };
 
@@ -32,41 +62,492 @@ __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
   return n;
 }
 
-// One warp per query row: lanes over the head's columns, keys one after the other with an online softmax.
-template <int D>
-__global__ void __launch_bounds__(128) fa_paged_decode_kernel(const PagedArgs a) {
-  constexpr int E = D / 32;
-  const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= static_cast<long long>(a.B) * a.H * a.N) return;
-  const int i = static_cast<int>(w % a.N), h = static_cast<int>(w / a.N % a.H), b = static_cast<int>(w / a.N / a.H);
-  const int n = paged_len(a, b);
-  const int end = a.causal ? min(n, n - a.N + i + 1) : n;
-  float q[E], acc[E];
-  for (int e = 0; e < E; ++e) {
-    q[e] = static_cast<float>(a.q[row_offset(a.sq, b, h, i) + lane * E + e]) * a.scale_log2;
-    acc[e] = 0.f;
+// D: head dim.  RM: query rows of a row tile (8, 16 or 32).
+template <int D_, int RM_>
+struct PagedCfg {
+  static constexpr int D = D_, RM = RM_;
+  static constexpr bool HALF = RM == 8;          // the lo parts of P in rows 8 .. 15
+  static constexpr int MT = HALF ? 1 : RM / 16;
+  static constexpr int KT = D == 64 ? 32 : 16;   // keys per tile
+  static constexpr int NT = KT / 8;
+  static constexpr int WARPS = 4, THREADS = 32 * WARPS;
+  static constexpr int STAGES = 3;
+  static constexpr int PITCH = 2 * D;            // bytes of a key in shared memory
+  static constexpr int TILE = KT * PITCH;
+  static constexpr int STAGE = 2 * TILE;         // K, then V
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int SMEM = WARPS * RING;
+  static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
+};
+constexpr int kPagedSms = 148;
+constexpr int kPagedMinTiles = 2;                // of a range: what is in flight at once
+
+// Rows of a row tile: rounded up to 8, 16 or (d < 256) 32.
+__host__ __device__ inline int paged_row_tile(int d, int rows) { return rows <= 8 ? 8 : rows <= 16 || d == 256 ? 16 : 32; }
+// Warps that share one row tile's work.
+__host__ __device__ inline int paged_workers(int d, int row_tiles) {
+  const int ctas = kPagedSms * (d == 256 ? 1 : 2) / row_tiles;
+  return (ctas < 1 ? 1 : ctas) * 4;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// c += a b: a 16 x 16 (row), b 16 x 8 (column), bf16; c fp32.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 bytes to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A place in the line of tiles: tile `tile` of the `tiles` of (sequence b, key/value head h).
+struct PagedPlace {
+  int b, h, tile, tiles, len;
+  template <int KT>
+  __device__ __forceinline__ void enter(const PagedArgs& a) {      // sequence b's length; empty ones have a tile too
+    len = b < a.B ? paged_len(a, b) : 0;
+    tiles = max(1, (len + KT - 1) / KT);
   }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < end; ++j) {
-    const int page = __ldg(a.table + b * a.table_stride + j / a.page);
-    if (page < 0 || page >= a.num_pages) {
-      atomicOr(a.status, DEV_ARGS);
-      break;
+  template <int KT>
+  __device__ __forceinline__ void next_pair(const PagedArgs& a) {
+    tile = 0;
+    if (++h == a.H_kv) {
+      h = 0;
+      ++b;
+      enter<KT>(a);
     }
-    const __nv_bfloat16* k = a.kp + row_offset(a.skp, page, h / a.group, j % a.page) + lane * E;
-    const __nv_bfloat16* v = a.vp + row_offset(a.svp, page, h / a.group, j % a.page) + lane * E;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], static_cast<float>(k[e]), s);
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), alpha = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * alpha + p;
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, static_cast<float>(v[e]), acc[e] * alpha);
-    m = mn;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int e = 0; e < E; ++e) a.o[row_offset(a.so, b, h, i) + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
-  if (lane == 0) a.lse[w] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+};
+
+template <int D, int RM>
+__global__ void __launch_bounds__(128, (PagedCfg<D, RM>::CTAS))
+fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
+  using C = PagedCfg<D, RM>;
+  constexpr int KT = C::KT, NT = C::NT, MT = C::MT, RW = C::HALF ? 1 : 2;   // RW: rows of a thread in a 16-row tile
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ long long before[C::THREADS + 1];
+  __shared__ long long warp_sum[C::WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int worker = blockIdx.x * C::WARPS + warp, rt = blockIdx.y;
+
+  // ---- the line: thread t sums the tiles of sequences t q .. t q + q - 1
+  const int per_thread = (a.B + C::THREADS - 1) / C::THREADS;
+  {
+    long long mine = 0;
+    for (int b = tid * per_thread; b < min(a.B, (tid + 1) * per_thread); ++b) mine += max(1, (paged_len(a, b) + KT - 1) / KT);
+    long long x = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long base = 0;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    before[tid] = base + x - mine;
+    if (tid == C::THREADS - 1) before[C::THREADS] = base + x;
+    __syncthreads();
+  }
+  const long long total = before[C::THREADS] * a.H_kv;
+  const long long share = (total + a.workers - 1) / a.workers;
+  const long long range = share > kPagedMinTiles ? share : kPagedMinTiles;
+  const long long t0 = range * worker, t1 = t0 + range < total ? t0 + range : total;
+  if (t0 >= t1) return;
+
+  // ---- where this warp's range begins
+  PagedPlace in;                                   // the next tile to load
+  long long pair0;                                 // first tile in the line of the pair that `in` is in
+  {
+    const long long s0 = t0 / a.H_kv;              // before[] counts tiles of one head
+    int slot = 0;
+#pragma unroll
+    for (int w = 0; w < C::WARPS; ++w) slot += __popc(__ballot_sync(0xffffffffu, before[32 * w + lane] <= s0));
+    in.b = (slot - 1) * per_thread;
+    long long base = before[slot - 1];
+    in.enter<KT>(a);
+    while (base + in.tiles <= s0) {                // at most per_thread steps
+      base += in.tiles;
+      ++in.b;
+      in.enter<KT>(a);
+    }
+    const long long rest = t0 - base * a.H_kv;     // below H_kv * tiles
+    in.h = static_cast<int>(rest / in.tiles);
+    in.tile = static_cast<int>(rest - static_cast<long long>(in.h) * in.tiles);
+    pair0 = t0 - in.tile;
+  }
+  PagedPlace at = in;                              // the next tile to use
+  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+
+  // ---- loading
+  const int groups_per_page = a.page / 8;
+  int pg_next = -1, row_next = 0, pg = -1, row_in = 0;   // this lane's 8 keys: page and first row; the next 256 keys'
+  int g0 = -1;                                     // first 8-key group of pg
+  auto look_up = [&](int g) {                      // page and row of 8-key group g + lane of pair `in`
+    const int mine = g + lane;
+    pg_next = -1;
+    row_next = 0;
+    if (8LL * mine < in.len) {
+      const int e = mine / groups_per_page;
+      row_next = (mine - e * groups_per_page) * 8;
+      pg_next = __ldg(a.table + in.b * a.table_stride + e);
+      if (pg_next < 0 || pg_next >= a.num_pages) {
+        atomicOr(a.status, DEV_ARGS);
+        pg_next = -1;
+      }
+    }
+  };
+  long long to_load = t1 - t0;
+  int load_stage = 0;
+  auto load_tile = [&]() {
+    if (to_load > 0) {
+      --to_load;
+      const int g = in.tile * (KT / 8);
+      if (g0 < 0 || g >= g0 + 32) {                // KT / 8 divides 32: a tile's groups are in one look-up
+        const int want = g & ~31;
+        if (g0 < 0) look_up(want);
+        pg = pg_next;
+        row_in = row_next;
+        g0 = want;
+        look_up(want + 32);
+      }
+      constexpr int CH = D / 8, RPI = 32 / CH;     // 16-byte chunks of a key; keys per warp copy
+      const uint32_t st = ring + load_stage * C::STAGE;
+      const int ch = lane % CH, r0 = lane / CH;
+#pragma unroll
+      for (int u = 0; u < KT / 8; ++u) {
+        const int p = __shfl_sync(0xffffffffu, pg, (g - g0) + u), row = __shfl_sync(0xffffffffu, row_in, (g - g0) + u);
+        const __nv_bfloat16* k = a.kp + (p < 0 ? 0 : row_offset(a.skp, p, in.h, row + r0) + ch * 8);
+        const __nv_bfloat16* v = a.vp + (p < 0 ? 0 : row_offset(a.svp, p, in.h, row + r0) + ch * 8);
+        const int left = p < 0 ? 0 : in.len - (g + u) * 8;     // keys of this group that exist
+        const long long ks = p < 0 ? 0 : a.skp.r * RPI, vs = p < 0 ? 0 : a.svp.r * RPI;
+#pragma unroll
+        for (int r = 0; r < 8; r += RPI) {
+          const int key = u * 8 + r + r0;
+          const bool real = r + r0 < left;
+          const uint32_t dst = st + key * C::PITCH + ((ch ^ (key & 7)) << 4);
+          copy16(dst, real ? k : a.kp, real);
+          copy16(dst + C::TILE, real ? v : a.vp, real);
+          k += ks;
+          v += vs;
+        }
+      }
+      if (++in.tile == in.tiles) {
+        if (to_load > 0) in.next_pair<KT>(a);
+        g0 = -1;
+      }
+      load_stage = load_stage + 1 == C::STAGES ? 0 : load_stage + 1;
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < C::STAGES - 1; ++s) load_tile();
+
+  // ---- a pair's rows: this thread's rows of the 16-row tiles are lane / 4 and (unless HALF) lane / 4 + 8
+  const int quad = lane & 3;
+  const float c2 = a.scale_log2;
+  uint32_t qf[MT][D / 16][C::HALF ? 2 : 4];
+  float acc[MT][D / 8][4];
+  float m[MT][RW], l[MT][RW];
+  int lim[MT][RW];                                 // last key the row sees
+  auto row_of = [&](int mt, int w) { return rt * RM + mt * 16 + w * 8 + (lane >> 2); };
+  auto begin_pair = [&]() {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int w = 0; w < RW; ++w) {
+        const int r = row_of(mt, w), g = r / a.N, i = r - g * a.N;
+        lim[mt][w] = a.causal ? at.len - a.N + i : at.len - 1;
+        m[mt][w] = -INFINITY;
+        l[mt][w] = 0.f;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            a.q + (r < a.rows ? row_offset(a.sq, at.b, at.h * a.group + g, i) : 0)) + quad;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[mt][k][w] = r < a.rows ? __ldg(src + 8 * k) : 0u;
+          qf[mt][k][RW + w] = r < a.rows ? __ldg(src + 8 * k + 4) : 0u;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.f;
+    }
+  };
+  auto end_pair = [&](bool begins, bool ends) {    // of the pair's tiles this warp had the first, the last
+    const long long slot = ((static_cast<long long>(rt) * a.workers + worker) * 2 + (begins ? 1 : 0)) * a.part_rows;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int w = 0; w < RW; ++w) {
+        float sum = l[mt][w];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = row_of(mt, w);
+        if (r >= a.rows) continue;
+        const int g = r / a.N, i = r - g * a.N, hq = at.h * a.group + g;
+        const float top = m[mt][w] == -INFINITY ? -INFINITY : m[mt][w] * c2;
+        if (begins && ends) {
+          const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+          __nv_bfloat16* o = a.o + row_offset(a.so, at.b, hq, i) + 2 * quad;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            const float x = C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w];
+            const float y = C::HALF ? acc[mt][n][1] + acc[mt][n][3] : acc[mt][n][2 * w + 1];
+            *reinterpret_cast<uint32_t*>(o + 8 * n) = pack_bf16x2(x * inv, y * inv);
+          }
+          if (quad == 0)
+            a.lse[(static_cast<long long>(at.b) * a.H + hq) * a.N + i] =
+                sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+        } else {
+          const long long pr = slot + r - rt * RM;
+          float* o = a.part_o + pr * D + 2 * quad;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            const float x = C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w];
+            const float y = C::HALF ? acc[mt][n][1] + acc[mt][n][3] : acc[mt][n][2 * w + 1];
+            *reinterpret_cast<float2*>(o + 8 * n) = make_float2(x, y);
+          }
+          if (quad == 0) a.part_ml[pr] = make_float2(top, sum);
+        }
+      }
+    if (begins && lane == 0) {
+      const int more = ends ? 0 : static_cast<int>((pair0 + at.tiles - 1) / range) - worker;
+      a.meta[(static_cast<long long>(rt) * a.B + at.b) * a.H_kv + at.h] = make_int2(worker, more);
+    }
+  };
+
+  begin_pair();
+  bool begins = at.tile == 0;
+  int stage = 0;
+  for (long long t = t0; t < t1; ++t) {
+    copy_wait<C::STAGES - 2>();
+    __syncwarp();                                  // everyone's copies of this tile; everyone is done with the last one
+    load_tile();
+    const uint32_t ks = ring + stage * C::STAGE, vs = ks + C::TILE;
+    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+    // ---- S = Q K^T
+    float s[MT][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+    {
+      const int row = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t kf[4];
+          ldsm4(ks + (row + 8 * n) * C::PITCH + (((2 * k + hi) ^ (row & 7)) << 4), kf);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint32_t a0 = qf[mt][k][0], a1 = C::HALF ? 0u : qf[mt][k][1], a2 = qf[mt][k][RW],
+                           a3 = C::HALF ? 0u : qf[mt][k][2 * RW - 1];
+            mma_bf16(s[mt][n], a0, a1, a2, a3, kf[0], kf[1]);
+            mma_bf16(s[mt][n + 1], a0, a1, a2, a3, kf[2], kf[3]);
+          }
+        }
+      }
+    }
+    // ---- masks: the tiles at the sequence's end
+    const int key0 = at.tile * KT + 2 * quad;
+    if ((at.tile + 1) * KT > at.len - (a.causal ? a.N - 1 : 0)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2 * RW; ++e)
+            if (key0 + 8 * n + (e & 1) > lim[mt][e >> 1]) s[mt][n][e] = -INFINITY;
+    }
+    // ---- online softmax
+    bool grew = false;
+    float alpha[MT][RW];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int w = 0; w < RW; ++w) {
+        float top = fmaxf(s[mt][0][2 * w], s[mt][0][2 * w + 1]);
+#pragma unroll
+        for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[mt][n][2 * w], s[mt][n][2 * w + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const bool grows = (top - m[mt][w]) * c2 > 8.0f;      // false while the row has seen no key
+        alpha[mt][w] = 1.0f;
+        if (grows) {
+          alpha[mt][w] = ex2_approx((m[mt][w] - top) * c2);
+          l[mt][w] *= alpha[mt][w];
+          m[mt][w] = top;
+          grew = true;
+        }
+        const float nb = m[mt][w] == -INFINITY ? 0.f : m[mt][w] * c2;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p = ex2_approx(fmaf(s[mt][n][2 * w + e], c2, -nb));
+            s[mt][n][2 * w + e] = p;
+            l[mt][w] += p;
+          }
+      }
+    if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[mt][n][e] *= alpha[mt][C::HALF ? 0 : e >> 1];
+    }
+    // ---- O += P V
+#pragma unroll
+    for (int kk = 0; kk < NT / 2; ++kk) {
+      uint32_t hi[MT][2 * RW], lo[MT][2 * RW];     // keys 0 .. 7 of the 16 (rows, rows + 8), then keys 8 .. 15
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int x = 0; x < 2 * RW; ++x) {
+          const float* p = &s[mt][2 * kk + x / RW][2 * (x % RW)];
+          hi[mt][x] = pack_bf16x2(p[0], p[1]);
+          const float2 h = bf16x2_to_float2(hi[mt][x]);
+          lo[mt][x] = pack_bf16x2(p[0] - h.x, p[1] - h.y);
+        }
+      const int row = 16 * kk + (lane & 15), c0 = lane >> 4;
+#pragma unroll
+      for (int n = 0; n < D / 8; n += 2) {
+        uint32_t vf[4];
+        ldsm4_t(vs + row * C::PITCH + (((n + c0) ^ (row & 7)) << 4), vf);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if constexpr (C::HALF) {
+            mma_bf16(acc[mt][n], hi[mt][0], lo[mt][0], hi[mt][1], lo[mt][1], vf[0], vf[1]);
+            mma_bf16(acc[mt][n + 1], hi[mt][0], lo[mt][0], hi[mt][1], lo[mt][1], vf[2], vf[3]);
+          } else {
+            mma_bf16(acc[mt][n], hi[mt][0], hi[mt][1], hi[mt][2], hi[mt][3], vf[0], vf[1]);
+            mma_bf16(acc[mt][n + 1], hi[mt][0], hi[mt][1], hi[mt][2], hi[mt][3], vf[2], vf[3]);
+            mma_bf16(acc[mt][n], lo[mt][0], lo[mt][1], lo[mt][2], lo[mt][3], vf[0], vf[1]);
+            mma_bf16(acc[mt][n + 1], lo[mt][0], lo[mt][1], lo[mt][2], lo[mt][3], vf[2], vf[3]);
+          }
+        }
+      }
+    }
+    const bool ends = ++at.tile == at.tiles;
+    if (ends || t + 1 == t1) {
+      end_pair(begins, ends);
+      if (t + 1 < t1) {
+        pair0 += at.tiles;
+        at.next_pair<KT>(a);
+        begin_pair();
+        begins = true;
+      }
+    }
+  }
+}
+
+// Joins the partials of the pairs that several warps shared: one warp per query row, or, when a row has more than 32
+// partials, the block's eight warps one row after the other.
+template <int D>
+__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedArgs a, int rm) {
+  constexpr int V = D / 32;                        // columns of a lane
+  __shared__ float so[8][D];
+  __shared__ float2 sml[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long rows = static_cast<long long>(a.B) * a.H * a.N;
+  const long long row0 = static_cast<long long>(blockIdx.x) * 8;
+
+  struct Row { int b, hq, i, worker, more; long long first; };
+  auto find = [&](long long row) {
+    Row r;
+    r.i = static_cast<int>(row % a.N);
+    r.hq = static_cast<int>(row / a.N % a.H);
+    r.b = static_cast<int>(row / a.N / a.H);
+    const int h = r.hq / a.group, rr = (r.hq - h * a.group) * a.N + r.i, rt = rr / rm;
+    const int2 mt = a.meta[(static_cast<long long>(rt) * a.B + r.b) * a.H_kv + h];
+    r.worker = mt.x;
+    r.more = mt.y;
+    r.first = (static_cast<long long>(rt) * a.workers + mt.x) * 2 * a.part_rows + rr - rt * rm;
+    return r;
+  };
+  // partial j of a row: the first lies in slot 1 of its worker, the others in slot 0 of the workers behind it
+  auto place = [&](const Row& r, int j) {
+    return r.first + (2LL * j + (j == 0 ? 1 : 0)) * a.part_rows;
+  };
+  float acc[V];
+  float m, l;
+  auto gather = [&](const Row& r, int from, int step) {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int j = from; j <= r.more; j += step) m = fmaxf(m, a.part_ml[place(r, j)].x);
+    const float nb = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int j = from; j <= r.more; j += step) {
+      const long long p = place(r, j);
+      const float2 ml = a.part_ml[p];
+      const float w = exp2f(ml.x - nb);
+      l = fmaf(w, ml.y, l);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, a.part_o[p * D + lane + 32 * e], acc[e]);
+    }
+  };
+  auto put = [&](const Row& r) {
+    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+    __nv_bfloat16* o = a.o + row_offset(a.so, r.b, r.hq, r.i);
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
+    if (lane == 0)
+      a.lse[(static_cast<long long>(r.b) * a.H + r.hq) * a.N + r.i] =
+          l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  };
+  constexpr int kAlone = 32;
+  if (row0 + warp < rows) {
+    const Row r = find(row0 + warp);
+    if (r.more > 0 && r.more < kAlone) {
+      gather(r, 0, 1);
+      put(r);
+    }
+  }
+  for (int x = 0; x < 8 && row0 + x < rows; ++x) {
+    const Row r = find(row0 + x);                  // the same for every thread
+    if (r.more < kAlone) continue;
+    gather(r, warp, 8);
+#pragma unroll
+    for (int e = 0; e < V; ++e) so[warp][lane + 32 * e] = acc[e];
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp == 0) {
+      float top = -INFINITY;
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, sml[w].x);
+      const float nb = top == -INFINITY ? 0.f : top;
+      m = top;
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = 0.f;
+      for (int w = 0; w < 8; ++w) {
+        const float f = exp2f(sml[w].x - nb);
+        l = fmaf(f, sml[w].y, l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(f, so[w][lane + 32 * e], acc[e]);
+      }
+      put(r);
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace fa

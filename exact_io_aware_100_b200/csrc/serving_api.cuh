@@ -44,9 +44,51 @@ fa_status check_paged(const fa_paged_layout& L) {
 fa_status check_decode(const fa_paged_layout& L) {
   const fa_status st = check_paged(L);
   if (st != FA_OK) return st;
-  if (L.N < 1 || L.H < 1 || L.H % L.H_kv != 0 || 1LL * L.B * L.H * L.N >= (1LL << 31)) return FA_ERR_INVALID;
+  if (L.N < 1 || L.H < 1 || L.H % L.H_kv != 0 || 1LL * L.B * L.H * L.N >= (1LL << 31) ||
+      1LL * (L.H / L.H_kv) * L.N >= (1LL << 19))
+    return FA_ERR_INVALID;
   if (!strides_ok(L.q, L.N, L.H, L.B) || !strides_ok(L.o, L.N, L.H, L.B)) return FA_ERR_ALIGN;
   return FA_OK;
+}
+
+// How a decode call is cut up, and where its workspace's parts lie.
+struct PagedPlan {
+  int rm, row_tiles, workers, part_rows;
+  size_t o_bytes, ml_bytes, meta_bytes;
+  size_t bytes() const { return o_bytes + ml_bytes + meta_bytes; }
+};
+PagedPlan paged_plan(const fa_paged_layout& L) {
+  PagedPlan p;
+  const int rows = L.H / L.H_kv * L.N;
+  p.rm = paged_row_tile(L.d, rows);
+  p.row_tiles = (rows + p.rm - 1) / p.rm;
+  p.part_rows = rows < p.rm ? rows : p.rm;
+  // no more warps than the longest sequences that the table can hold give work to
+  const int kt = L.d == 64 ? 32 : 16;
+  const long long tiles = (1LL * L.max_pages * L.page_size + kt - 1) / kt * L.B * L.H_kv;
+  const long long ctas = (tiles + 4 * kPagedMinTiles - 1) / (4 * kPagedMinTiles);
+  p.workers = paged_workers(L.d, p.row_tiles);
+  if (ctas < p.workers / 4) p.workers = static_cast<int>(ctas) * 4;
+  const size_t parts = 2 * static_cast<size_t>(p.row_tiles) * p.workers * p.part_rows;
+  p.o_bytes = round256(parts * L.d * 4);
+  p.ml_bytes = round256(parts * 8);
+  p.meta_bytes = round256(8 * static_cast<size_t>(p.row_tiles) * L.B * L.H_kv);
+  return p;
+}
+
+template <int D, int RM>
+fa_status launch_paged(const PagedArgs& a, bool* attr, cudaStream_t s) {
+  using C = PagedCfg<D, RM>;
+  if (!*attr) {
+    if (cudaFuncSetAttribute(fa_paged_decode_kernel<D, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+      return FA_ERR_CUDA;
+    *attr = true;
+  }
+  fa_paged_decode_kernel<D, RM><<<dim3(a.workers / C::WARPS, a.row_tiles), C::THREADS, C::SMEM, s>>>(a);
+  const long long rows = 1LL * a.B * a.H * a.N;
+  fa_paged_merge_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a, RM);
+  return launched();
 }
 
 bool pages_layout_ok(const fa_pages_layout* L) {
@@ -199,7 +241,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
 
 size_t fa_paged_decode_workspace_size(const fa_paged_layout* layout) {
   if (layout == nullptr || check_decode(*layout) != FA_OK) return 0;
-  return 256;
+  return paged_plan(*layout).bytes();
 }
 
 fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -213,7 +255,8 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned_to(lse, 4) ||
       !aligned_to(page_table, 4) || !aligned_to(seq_lens, 4))
     return FA_ERR_ALIGN;
-  if (!workspace_ok(workspace, workspace_bytes, fa_paged_decode_workspace_size(layout))) return FA_ERR_WORKSPACE;
+  const PagedPlan plan = paged_plan(L);
+  if (!workspace_ok(workspace, workspace_bytes, plan.bytes())) return FA_ERR_WORKSPACE;
   DevState* ds = nullptr;
   if ((st = device_state(&ds)) != FA_OK) return st;
   PagedArgs a = {};
@@ -240,12 +283,27 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   a.causal = causal ? 1 : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = ds->status;
+  a.rows = a.group * a.N;
+  a.workers = plan.workers;
+  a.row_tiles = plan.row_tiles;
+  a.part_rows = plan.part_rows;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.part_o = reinterpret_cast<float*>(w);
+  a.part_ml = reinterpret_cast<float2*>(w + plan.o_bytes);
+  a.meta = reinterpret_cast<int2*>(w + plan.o_bytes + plan.ml_bytes);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned blocks = static_cast<unsigned>((1LL * L.B * L.H * L.N + 3) / 4);
-  if (L.d == 64) fa_paged_decode_kernel<64><<<blocks, 128, 0, s>>>(a);
-  else if (L.d == 128) fa_paged_decode_kernel<128><<<blocks, 128, 0, s>>>(a);
-  else fa_paged_decode_kernel<256><<<blocks, 128, 0, s>>>(a);
-  return launched();
+  const int di = L.d == 64 ? 0 : L.d == 128 ? 1 : 2, ri = plan.rm == 8 ? 0 : plan.rm == 16 ? 1 : 2;
+  bool* attr = &ds->paged_attr[di][ri];
+  switch (di * 3 + ri) {
+    case 0: return launch_paged<64, 8>(a, attr, s);
+    case 1: return launch_paged<64, 16>(a, attr, s);
+    case 2: return launch_paged<64, 32>(a, attr, s);
+    case 3: return launch_paged<128, 8>(a, attr, s);
+    case 4: return launch_paged<128, 16>(a, attr, s);
+    case 5: return launch_paged<128, 32>(a, attr, s);
+    case 6: return launch_paged<256, 8>(a, attr, s);
+    default: return launch_paged<256, 16>(a, attr, s);
+  }
 }
 
 size_t fa_pages_workspace_size(const fa_pages_layout* layout, int n) {

@@ -325,7 +325,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
  * lse: dense [B, H, N] float.
  * causal != 0: query i sees keys j <= seq_lens[b] - N + i.  Otherwise the
  * definition of fa_decode; a query that sees no key (an empty sequence, or N >
- * seq_lens[b]) gets o = 0, lse = -inf.  H a multiple of H_kv; N >= 1.  What
+ * seq_lens[b]) gets o = 0, lse = -inf.  H a multiple of H_kv; N >= 1, H / H_kv * N < 2^19.  What
  * the pages hold behind a sequence's end does not matter (NaN included); a key
  * that only some of the N queries see has to be finite.
  * workspace: at least fa_paged_decode_workspace_size(layout) bytes, 256-byte
