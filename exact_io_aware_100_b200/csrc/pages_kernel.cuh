@@ -281,32 +281,49 @@ struct PageCopyArgs {
   Strides sk, sv;                  // {page, head, row}
   const int* copies;
   int n, P, page, H_kv, d;
+  int tpr;                         // threads of a row
+  int rows_per, row_parts;         // a head's rows are copied in row_parts parts of rows_per
   uint32_t* status;
 };
+constexpr int kPageCopyBytes = 16384;   // of a part: four 16-byte vectors in flight per thread
 
-// Block x takes rows x, x + grid, ... of the list: its lanes look at 32 of them at once, so a list that is mostly empty
-// costs one read, and its threads copy the listed page's rows, 16 bytes at a time, K then V.
+// A copy is cut into parts (K or V, a head, a piece of its rows).  Block = (team, part): the block copies its part of the
+// list's rows team, team + teams, ...; its lanes look at 32 of them at once, so a list that is mostly empty costs one
+// read.  16 bytes at a time, a thread has a fixed column.
 __global__ void __launch_bounds__(256) fa_pages_copy_kernel(const PageCopyArgs a) {
-  const int vecs = a.d / 8, lane = threadIdx.x & 31;
-  for (long long base = blockIdx.x; base < a.n; base += 32LL * gridDim.x) {
-    const long long mine = base + static_cast<long long>(lane) * gridDim.x;
+  const int lane = threadIdx.x & 31;
+  const int parts = 2 * a.H_kv * a.row_parts, teams = gridDim.x / parts;
+  const int team = blockIdx.x / parts, part = blockIdx.x - team * parts;
+  const int hk = part / a.row_parts, piece = part - hk * a.row_parts;
+  const bool is_v = hk >= a.H_kv;
+  const Strides st = is_v ? a.sv : a.sk;
+  __nv_bfloat16* base = (is_v ? a.vp : a.kp) + (hk - (is_v ? a.H_kv : 0)) * st.h;
+  const int step = 256 / a.tpr, row0 = threadIdx.x / a.tpr, x0 = 8 * (threadIdx.x - row0 * a.tpr);
+  const int first = piece * a.rows_per;
+  for (long long at = team; at < a.n; at += 32LL * teams) {
+    const long long mine = at + static_cast<long long>(lane) * teams;
     unsigned todo = __ballot_sync(0xffffffffu, mine < a.n && __ldg(a.copies + 3 * mine) >= 0);
     for (; todo; todo &= todo - 1) {
-      const int* c = a.copies + 3 * (base + static_cast<long long>(__ffs(todo) - 1) * gridDim.x);
+      const int* c = a.copies + 3 * (at + static_cast<long long>(__ffs(todo) - 1) * teams);
       const int src = __ldg(c), dst = __ldg(c + 1), rows = __ldg(c + 2);
       if (src >= a.P || dst < 0 || dst >= a.P || rows < 0 || rows > a.page) {
         if (threadIdx.x == 0) atomicOr(a.status, DEV_ARGS);
         continue;
       }
-      const int per = rows * vecs;
-      for (int e = threadIdx.x; e < 2 * a.H_kv * per; e += 256) {
-        const int hk = e / per, r = e - hk * per, row = r / vecs, x = r - row * vecs;
-        const bool k = hk < a.H_kv;
-        __nv_bfloat16* p = k ? a.kp : a.vp;
-        const Strides& st = k ? a.sk : a.sv;
-        const int h = k ? hk : hk - a.H_kv;
-        *reinterpret_cast<uint4*>(p + row_offset(st, dst, h, row) + 8 * x) =
-            *reinterpret_cast<const uint4*>(p + row_offset(st, src, h, row) + 8 * x);
+      if (row0 >= step) continue;                  // 256 is no multiple of tpr: the last threads have no row
+      const int end = min(rows, first + a.rows_per);
+      const __nv_bfloat16* from = base + src * st.b;
+      __nv_bfloat16* to = base + dst * st.b;
+      for (int x = x0; x < a.d; x += 8 * a.tpr) {
+        for (int r = first + row0; r < end; r += 4 * step) {
+          uint4 w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (r + u * step < end) w[u] = *reinterpret_cast<const uint4*>(from + (r + u * step) * st.r + x);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (r + u * step < end) *reinterpret_cast<uint4*>(to + (r + u * step) * st.r + x) = w[u];
+        }
       }
     }
   }

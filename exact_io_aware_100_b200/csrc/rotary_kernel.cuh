@@ -114,51 +114,168 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
   }
 }
 
-// One thread per (token, pair of columns), any alignment: thread p of a token takes pair p of the r / 2, or column
-// r + (p - r / 2) of those that are copied, in every head.
+// Heads hh of a launch: q's first, then k's, then (append) v's.
+struct RotHead {
+  const void* src;
+  void* dst;
+  bool turned;
+};
 template <typename T, bool APPEND>
-__global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a, int interleaved) {
+__device__ __forceinline__ RotHead rot_head(const RotArgs& a, const RotToken& tk, int hh) {
+  const int bc = APPEND && a.cu ? 0 : tk.b;
+  const int ob = APPEND ? tk.page : bc, orow = APPEND ? tk.in_page : tk.row;   // where k and v go
+  if (hh < a.H)
+    return {static_cast<const T*>(a.q) + row_offset(a.sq, bc, hh, tk.row),
+            static_cast<T*>(a.qo) + row_offset(a.sqo, bc, hh, tk.row), true};
+  const int h = hh - a.H;
+  if (!APPEND || h < a.H_kv)
+    return {static_cast<const T*>(a.k) + row_offset(a.sk, bc, h, tk.row),
+            static_cast<T*>(a.ko) + row_offset(a.sko, ob, h, orow), true};
+  return {static_cast<const T*>(a.v) + row_offset(a.sv, bc, h - a.H_kv, tk.row),
+          static_cast<T*>(a.vo) + row_offset(a.svo, ob, h - a.H_kv, orow), false};
+}
+
+// The pair of elements (xa, xb) turned.
+__device__ __forceinline__ float2 rot_turn(float xa, float xb, float2 cs) {
+  return make_float2(xa * cs.x - xb * cs.y, xb * cs.x + xa * cs.y);
+}
+
+// Any alignment and any even r: one thread per (token, pair of columns, chunk of heads); thread p of a token takes pair
+// p of the r / 2, or column r + (p - r / 2) of those that are copied.
+template <typename T, bool APPEND>
+__global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a, int interleaved, int heads_per) {
   const int half = a.r / 2, per = half + a.d - a.r;
   const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   const long long t = idx / per;
   if (t >= a.tokens) return;
   const int p = static_cast<int>(idx - t * per);
   const RotToken tk = rot_token<APPEND>(a, t);
-  const bool turn = p < half, pad = APPEND && (tk.skip || tk.page < 0);
+  const bool turn = p < half;
   const int ca = turn ? (interleaved ? 2 * p : p) : p + half, cb = turn ? (interleaved ? 2 * p + 1 : p + half) : ca;
   const float2 cs = turn ? rot_cos_sin(__ldg(a.freqs + p), tk.pos, a.magnitude, a.inverse) : make_float2(1.f, 0.f);
-  const int bc = APPEND && a.cu ? 0 : tk.b;
-  auto move = [&](const void* src, const Strides& ss, int sb, int srow, void* dst, const Strides& sd, int db, int drow,
-                  int heads, bool turned) {
-    for (int h = 0; h < heads; ++h) {
-      const T* x = static_cast<const T*>(src) + row_offset(ss, sb, h, srow);
-      T* y = static_cast<T*>(dst) + row_offset(sd, db, h, drow);
+  const bool pad = APPEND && (tk.skip || tk.page < 0);
+  const int heads = pad ? (tk.skip && a.qo == a.q ? 0 : a.H) : a.H + (APPEND ? 2 : 1) * a.H_kv;
+  const int h1 = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per);
+  for (int hh = blockIdx.y * heads_per; hh < h1; ++hh) {
+    const RotHead r = rot_head<T, APPEND>(a, tk, hh);
+    const T* x = static_cast<const T*>(r.src);
+    T* y = static_cast<T*>(r.dst);
+    if (pad) {
+      rot_store(y + ca, 0.f);
+      rot_store(y + cb, 0.f);
+    } else if (!turn || !r.turned) {
       const T va = x[ca], vb = x[cb];
-      if (!turn || !turned) {
-        y[ca] = va;
-        y[cb] = vb;
-      } else {
-        const float xa = static_cast<float>(va), xb = static_cast<float>(vb);
-        rot_store(y + ca, xa * cs.x - xb * cs.y);
-        rot_store(y + cb, xb * cs.x + xa * cs.y);
+      y[ca] = va;
+      y[cb] = vb;
+    } else {
+      const float2 z = rot_turn(rot_load(x + ca), rot_load(x + cb), cs);
+      rot_store(y + ca, z.x);
+      rot_store(y + cb, z.y);
+    }
+  }
+}
+
+// V elements of T (16 or 8 bytes) as floats, and back (to nearest even).
+template <typename T, int V>
+struct RotVec;
+template <int V_>
+struct RotVec<__nv_bfloat16, V_> {
+  struct __align__(2 * V_) Word { uint32_t u[V_ / 2]; };
+  __device__ static __forceinline__ void unpack(const Word& w, float (&x)[V_]) {
+#pragma unroll
+    for (int e = 0; e < V_ / 2; ++e) {
+      const float2 f = bf16x2_to_float2(w.u[e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  }
+  __device__ static __forceinline__ Word pack(const float (&x)[V_]) {
+    Word w;
+#pragma unroll
+    for (int e = 0; e < V_ / 2; ++e) w.u[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+    return w;
+  }
+};
+template <int V_>
+struct RotVec<float, V_> {
+  struct __align__(4 * V_) Word { uint32_t u[V_]; };
+  __device__ static __forceinline__ void unpack(const Word& w, float (&x)[V_]) {
+#pragma unroll
+    for (int e = 0; e < V_; ++e) x[e] = __uint_as_float(w.u[e]);
+  }
+  __device__ static __forceinline__ Word pack(const float (&x)[V_]) {
+    Word w;
+#pragma unroll
+    for (int e = 0; e < V_; ++e) w.u[e] = __float_as_uint(x[e]);
+    return w;
+  }
+};
+
+// The vector path: aligned rows whose turned columns, and the others, fall into whole pairs of vectors of V elements (r
+// and d multiples of 2 V).  A thread takes two vectors of a token, forms
+// their angles once, and turns them in `heads_per` heads, kHeads of them in flight; its other work is the copying of
+// columns r .. d - 1, two vectors too.
+template <typename T, int V, bool APPEND, bool INTER>
+__global__ void __launch_bounds__(256) fa_rotary_vec_kernel(const __grid_constant__ RotArgs a, int heads_per) {
+  using R = RotVec<T, V>;
+  using Word = typename R::Word;
+  constexpr int kHeads = 4;
+  const int per = a.d / (2 * V), turning = a.r / (2 * V);      // items of a token, of which these turn
+  const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long t = idx / per;
+  if (t >= a.tokens) return;
+  const int p = static_cast<int>(idx - t * per);
+  const RotToken tk = rot_token<APPEND>(a, t);
+  const bool turn = p < turning;
+  // columns of the two vectors
+  const int ca = INTER || !turn ? 2 * V * p : V * p, cb = INTER || !turn ? ca + V : ca + a.r / 2;
+  float2 cs[V];                    // half layout: of column ca + e; interleaved: of pair ca / 2 + e
+  if (turn) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) cs[e] = rot_cos_sin(__ldg(a.freqs + V * p + e), tk.pos, a.magnitude, a.inverse);
+  }
+  const bool pad = APPEND && (tk.skip || tk.page < 0);
+  const int heads = pad ? (tk.skip && a.qo == a.q ? 0 : a.H) : a.H + (APPEND ? 2 : 1) * a.H_kv;
+  const int h1 = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per);
+  for (int h0 = blockIdx.y * heads_per; h0 < h1; h0 += kHeads) {
+    Word va[kHeads], vb[kHeads];
+    T* dst[kHeads];
+    bool act[kHeads];
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+      va[u] = vb[u] = Word{};
+      if (h0 + u < h1) {
+        const RotHead r = rot_head<T, APPEND>(a, tk, h0 + u);
+        const T* x = static_cast<const T*>(r.src);
+        dst[u] = static_cast<T*>(r.dst);
+        act[u] = turn && r.turned && !pad;
+        if (!pad) {
+          va[u] = *reinterpret_cast<const Word*>(x + ca);
+          vb[u] = *reinterpret_cast<const Word*>(x + cb);
+        }
       }
     }
-  };
-  if (pad) {
-    if (a.q && !(tk.skip && a.qo == a.q))
-      for (int h = 0; h < a.H; ++h) {
-        T* y = static_cast<T*>(a.qo) + row_offset(a.sqo, bc, h, tk.row);
-        rot_store(y + ca, 0.f);
-        rot_store(y + cb, 0.f);
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+      if (h0 + u >= h1) break;
+      if (act[u]) {
+        float xa[V], xb[V];
+        R::unpack(va[u], xa);
+        R::unpack(vb[u], xb);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float& fa = INTER ? (e < V / 2 ? xa[2 * e] : xb[2 * e - V]) : xa[e];
+          float& fb = INTER ? (e < V / 2 ? xa[2 * e + 1] : xb[2 * e + 1 - V]) : xb[e];
+          const float2 z = rot_turn(fa, fb, cs[e]);
+          fa = z.x;
+          fb = z.y;
+        }
+        va[u] = R::pack(xa);
+        vb[u] = R::pack(xb);
       }
-    return;
-  }
-  if (a.q) move(a.q, a.sq, bc, tk.row, a.qo, a.sqo, bc, tk.row, a.H, true);
-  if (APPEND) {
-    move(a.k, a.sk, bc, tk.row, a.ko, a.sko, tk.page, tk.in_page, a.H_kv, true);
-    move(a.v, a.sv, bc, tk.row, a.vo, a.svo, tk.page, tk.in_page, a.H_kv, false);
-  } else if (a.H_kv > 0) {
-    move(a.k, a.sk, bc, tk.row, a.ko, a.sko, bc, tk.row, a.H_kv, true);
+      *reinterpret_cast<Word*>(dst[u] + ca) = va[u];
+      *reinterpret_cast<Word*>(dst[u] + cb) = vb[u];
+    }
   }
 }
 

@@ -2,6 +2,8 @@
 // Included behind fa_api.cu, whose device state and checks it uses.
 #pragma once
 
+#include <algorithm>
+
 #include "pages_kernel.cuh"
 #include "paged_decode_kernel.cuh"
 #include "rotary_kernel.cuh"
@@ -20,12 +22,40 @@ bool out_strides_ok(const fa_strides& st, int batch, int heads, int rows) {
   return (batch <= 1 || st.batch > 0) && (heads <= 1 || st.head > 0) && (rows <= 1 || st.row > 0);
 }
 
+// Can every row of the operand be moved in vectors of `bytes`?
+bool vec_rows(const void* p, const Strides& st, int batch, int heads, int rows, long long bytes, long long es) {
+  auto ok = [=](long long x, int extent) { return extent <= 1 || x * es % bytes == 0; };
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ok(st.b, batch) && ok(st.h, heads) && ok(st.r, rows);
+}
+
+// heads_per: heads of a thread.  A thread forms its angles once for all of its heads, so many heads save arithmetic, and
+// few give the GPU more threads to hide latency with: as many heads as leave kRotaryThreads threads, 4 to 16.
+constexpr long long kRotaryThreads = 148LL * 2048 * 2;
 template <typename T, bool APPEND>
 fa_status launch_rotary(const RotArgs& a, int interleaved, cudaStream_t stream) {
-  const long long per = a.r / 2 + a.d - a.r;
+  constexpr int es = sizeof(T), V = 16 / es;
+  const int heads = a.H + (APPEND ? 2 : 1) * a.H_kv;
+  const int rows = APPEND && a.cu != nullptr ? a.total : a.N, nb = APPEND && a.cu != nullptr ? 1 : a.B;
+  auto fits = [&](int v) {
+    auto rows_ok = [&](const void* p, const Strides& st, int h) { return vec_rows(p, st, nb, h, rows, v * es, es); };
+    return a.d % (2 * v) == 0 && a.r % (2 * v) == 0 && (a.H == 0 || (rows_ok(a.q, a.sq, a.H) && rows_ok(a.qo, a.sqo, a.H))) &&
+           (a.H_kv == 0 || APPEND || (rows_ok(a.k, a.sk, a.H_kv) && rows_ok(a.ko, a.sko, a.H_kv)));
+  };
+  const int v = fits(V) ? V : es == 2 && fits(4) ? 4 : 0;
+  const long long per = v ? a.d / (2 * v) : a.r / 2 + a.d - a.r;
   const long long blocks = (a.tokens * per + 255) / 256;
   if (blocks >= (1LL << 31)) return FA_ERR_INVALID;
-  fa_rotary_kernel<T, APPEND><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, interleaved);
+  const long long most = blocks * 256 * heads / kRotaryThreads, least = heads / 65535 + 1;
+  const int heads_per = static_cast<int>(std::max(std::min(std::max(most, 4LL), 16LL), least));
+  const dim3 grid(static_cast<unsigned>(blocks), (heads + heads_per - 1) / heads_per);
+  if (v == 0)
+    fa_rotary_kernel<T, APPEND><<<grid, 256, 0, stream>>>(a, interleaved, heads_per);
+  else if (v == V)
+    (interleaved ? fa_rotary_vec_kernel<T, V, APPEND, true> : fa_rotary_vec_kernel<T, V, APPEND, false>)
+        <<<grid, 256, 0, stream>>>(a, heads_per);
+  else
+    (interleaved ? fa_rotary_vec_kernel<T, 4, APPEND, true> : fa_rotary_vec_kernel<T, 4, APPEND, false>)
+        <<<grid, 256, 0, stream>>>(a, heads_per);
   return launched();
 }
 
@@ -147,7 +177,7 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
                     fa_dtype dtype, fa_stream_t stream) {
   if (layout == nullptr) return FA_ERR_INVALID;
   const fa_rotary_layout& L = *layout;
-  if (L.B < 1 || L.H < 1 || L.H_kv < 0 || L.N < 0 || L.d < 1 || L.d > 1024 || L.rotary_dim < 0 || L.rotary_dim > L.d ||
+  if (L.B < 1 || L.H < 1 || L.H_kv < 0 || L.H >= (1 << 24) || L.H_kv >= (1 << 24) || L.N < 0 || L.d < 1 || L.d > 1024 || L.rotary_dim < 0 || L.rotary_dim > L.d ||
       L.rotary_dim % 2 != 0 || 1LL * L.B * L.N >= (1LL << 31) || !std::isfinite(magnitude) ||
       !out_strides_ok(L.q_out, L.B, L.H, L.N) || (L.H_kv > 0 && !out_strides_ok(L.k_out, L.B, L.H_kv, L.N)))
     return FA_ERR_INVALID;
@@ -192,7 +222,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
   if (st != FA_OK) return st;
   const bool pk = L.cu_seqlens != nullptr;
   const long long tokens = pk ? L.total : 1LL * L.B * L.N;
-  if ((pk ? L.total : L.N) < 0 || tokens >= (1LL << 31) || (q != nullptr && L.H < 1) || !std::isfinite(magnitude) ||
+  if ((pk ? L.total : L.N) < 0 || tokens >= (1LL << 31) || (q != nullptr && (L.H < 1 || L.H >= (1 << 24))) || L.H_kv >= (1 << 24) || !std::isfinite(magnitude) ||
       (freqs != nullptr && (L.rotary_dim < 0 || L.rotary_dim > L.d || L.rotary_dim % 2 != 0)))
     return FA_ERR_INVALID;
   if (tokens == 0) return FA_OK;
@@ -392,8 +422,16 @@ fa_status fa_pages_copy(void* k_pages, void* v_pages, const int32_t* copies, int
   a.H_kv = L.H_kv;
   a.d = L.d;
   a.status = ds->status;
-  const int grid = n < ds->sms * 8 ? n : ds->sms * 8;
-  fa_pages_copy_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  a.tpr = std::min(L.d / 8, 256);
+  // parts of a copy: about kPageCopyBytes each, a head of K or V at most
+  const long long unit = 2LL * L.page_size * L.d;
+  const int want = static_cast<int>((unit + kPageCopyBytes - 1) / kPageCopyBytes);
+  a.rows_per = (L.page_size + want - 1) / want;
+  a.row_parts = (L.page_size + a.rows_per - 1) / a.rows_per;
+  const long long parts = 2LL * L.H_kv * a.row_parts;
+  const long long teams = std::max(1LL, std::min<long long>(n, ds->sms * 16LL / parts));
+  if (teams * parts >= (1LL << 31)) return FA_ERR_INVALID;
+  fa_pages_copy_kernel<<<static_cast<unsigned>(teams * parts), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
 
