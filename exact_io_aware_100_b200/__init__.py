@@ -125,6 +125,9 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int:
     import torch
     if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # 0.1 us; current_stream builds an object: 3 us
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

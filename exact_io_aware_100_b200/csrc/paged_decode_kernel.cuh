@@ -13,7 +13,8 @@
 //    the cut ones leave (max, sum, O) partials that the merge kernel joins.  The
 //    lengths are read on the device: a captured call follows them;
 //  * a warp fills its own ring of tiles with 16-byte asynchronous copies, across the
-//    ends of pairs, and waits for nobody: no block barrier in the loop.  A tile is
+//    ends of pairs, and waits for nobody: no block barrier in the loop.  Beginning and
+//    ending a pair (its rows' loads, its outputs) counts as kPagedPairUnits tiles.  A tile is
 //    gathered 8 keys at a time (8 divides the page size), and the page numbers of 256
 //    keys are read ahead.  Keys behind the sequence's end are filled with zeros in
 //    shared memory, so what the pages hold there does not matter;
@@ -44,6 +45,7 @@ struct PagedArgs {
   int causal;
   float scale_log2;
   int workers;                     // warps that share the work of one row tile
+  int min_units;                   // least units of a warp's range
   int row_tiles;
   int part_rows;                   // rows of a partial
   float* part_o;                   // [row tile][worker][2][part_rows][D]
@@ -80,7 +82,8 @@ struct PagedCfg {
   static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
 };
 constexpr int kPagedSms = 148;
-constexpr int kPagedMinTiles = 2;                // of a range: what is in flight at once
+constexpr int kPagedMinUnits = 2;                // of a range: what is in flight at once
+constexpr int kPagedPairUnits = 2;               // what beginning and ending a pair costs, in tiles
 
 // Rows of a row tile: rounded up to 8, 16 or (d < 256) 32.
 __host__ __device__ inline int paged_row_tile(int d, int rows) { return rows <= 8 ? 8 : rows <= 16 || d == 256 ? 16 : 32; }
@@ -113,8 +116,9 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A place in the line of tiles: tile `tile` of the `tiles` of (sequence b, key/value head h).
+// A place in the line: tile `tile` of the `tiles` of (sequence b, key/value head h), which is `unit` of the line.
 struct PagedPlace {
+  long long unit;
   int b, h, tile, tiles, len;
   template <int KT>
   __device__ __forceinline__ void enter(const PagedArgs& a) {      // sequence b's length; empty ones have a tile too
@@ -122,8 +126,9 @@ struct PagedPlace {
     tiles = max(1, (len + KT - 1) / KT);
   }
   template <int KT>
-  __device__ __forceinline__ void next_pair(const PagedArgs& a) {
+  __device__ __forceinline__ void next_pair(const PagedArgs& a) {  // unit: already behind this pair's last tile
     tile = 0;
+    unit += kPagedPairUnits;
     if (++h == a.H_kv) {
       h = 0;
       ++b;
@@ -142,12 +147,14 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   __shared__ long long warp_sum[C::WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int worker = blockIdx.x * C::WARPS + warp, rt = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge kernel may come up, and waits for the end
 
-  // ---- the line: thread t sums the tiles of sequences t q .. t q + q - 1
+  // ---- the line, of one head: thread t sums the units of sequences t q .. t q + q - 1
   const int per_thread = (a.B + C::THREADS - 1) / C::THREADS;
   {
     long long mine = 0;
-    for (int b = tid * per_thread; b < min(a.B, (tid + 1) * per_thread); ++b) mine += max(1, (paged_len(a, b) + KT - 1) / KT);
+    for (int b = tid * per_thread; b < min(a.B, (tid + 1) * per_thread); ++b)
+      mine += max(1, (paged_len(a, b) + KT - 1) / KT) + kPagedPairUnits;
     long long x = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -163,38 +170,40 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   }
   const long long total = before[C::THREADS] * a.H_kv;
   const long long share = (total + a.workers - 1) / a.workers;
-  const long long range = share > kPagedMinTiles ? share : kPagedMinTiles;
+  const long long range = share > a.min_units ? share : a.min_units;
   const long long t0 = range * worker, t1 = t0 + range < total ? t0 + range : total;
   if (t0 >= t1) return;
 
-  // ---- where this warp's range begins
+  // ---- the first tile at or behind t0
   PagedPlace in;                                   // the next tile to load
-  long long pair0;                                 // first tile in the line of the pair that `in` is in
   {
-    const long long s0 = t0 / a.H_kv;              // before[] counts tiles of one head
+    const long long s0 = t0 / a.H_kv;
     int slot = 0;
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) slot += __popc(__ballot_sync(0xffffffffu, before[32 * w + lane] <= s0));
     in.b = (slot - 1) * per_thread;
     long long base = before[slot - 1];
     in.enter<KT>(a);
-    while (base + in.tiles <= s0) {                // at most per_thread steps
-      base += in.tiles;
+    while (base + in.tiles + kPagedPairUnits <= s0) {   // at most per_thread steps
+      base += in.tiles + kPagedPairUnits;
       ++in.b;
       in.enter<KT>(a);
     }
-    const long long rest = t0 - base * a.H_kv;     // below H_kv * tiles
-    in.h = static_cast<int>(rest / in.tiles);
-    in.tile = static_cast<int>(rest - static_cast<long long>(in.h) * in.tiles);
-    pair0 = t0 - in.tile;
+    const long long rest = t0 - base * a.H_kv;     // of this sequence's H_kv (tiles + kPagedPairUnits)
+    const long long units = in.tiles + kPagedPairUnits;
+    in.h = static_cast<int>(rest / units);
+    const int u = static_cast<int>(rest - in.h * units) - kPagedPairUnits;
+    in.tile = max(0, u);
+    in.unit = t0 + in.tile - u;
   }
+  if (in.unit >= t1) return;
   PagedPlace at = in;                              // the next tile to use
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
 
   // ---- loading
   const int groups_per_page = a.page / 8;
   int pg_next = -1, row_next = 0, pg = -1, row_in = 0;   // this lane's 8 keys: page and first row; the next 256 keys'
-  int g0 = -1;                                     // first 8-key group of pg
+  int g0 = -1;                                     // first 8-key group of pg, in sequence in.b
   auto look_up = [&](int g) {                      // page and row of 8-key group g + lane of pair `in`
     const int mine = g + lane;
     pg_next = -1;
@@ -209,15 +218,12 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       }
     }
   };
-  long long to_load = t1 - t0;
   int load_stage = 0;
   auto load_tile = [&]() {
-    if (to_load > 0) {
-      --to_load;
-      const int g = in.tile * (KT / 8);
-      if (g0 < 0 || g >= g0 + 32) {                // KT / 8 divides 32: a tile's groups are in one look-up
-        const int want = g & ~31;
-        if (g0 < 0) look_up(want);
+    if (in.unit < t1) {
+      const int g = in.tile * (KT / 8), want = g & ~31;
+      if (want != g0) {                            // KT / 8 divides 32: a tile's groups are in one look-up
+        if (g0 < 0 || want != g0 + 32) look_up(want);
         pg = pg_next;
         row_in = row_next;
         g0 = want;
@@ -244,9 +250,13 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
           v += vs;
         }
       }
-      if (++in.tile == in.tiles) {
-        if (to_load > 0) in.next_pair<KT>(a);
-        g0 = -1;
+      ++in.unit;
+      if (++in.tile == in.tiles && in.unit + kPagedPairUnits < t1) {
+        const int b = in.b;
+        in.next_pair<KT>(a);
+        if (in.b != b) g0 = -1;
+      } else if (in.tile == in.tiles) {
+        in.unit = t1;
       }
       load_stage = load_stage + 1 == C::STAGES ? 0 : load_stage + 1;
     }
@@ -324,7 +334,7 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         }
       }
     if (begins && lane == 0) {
-      const int more = ends ? 0 : static_cast<int>((pair0 + at.tiles - 1) / range) - worker;
+      const int more = ends ? 0 : static_cast<int>((at.unit + at.tiles - 1 - at.tile) / range) - worker;
       a.meta[(static_cast<long long>(rt) * a.B + at.b) * a.H_kv + at.h] = make_int2(worker, more);
     }
   };
@@ -332,7 +342,7 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   begin_pair();
   bool begins = at.tile == 0;
   int stage = 0;
-  for (long long t = t0; t < t1; ++t) {
+  while (true) {
     copy_wait<C::STAGES - 2>();
     __syncwarp();                                  // everyone's copies of this tile; everyone is done with the last one
     load_tile();
@@ -445,109 +455,103 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         }
       }
     }
-    const bool ends = ++at.tile == at.tiles;
-    if (ends || t + 1 == t1) {
-      end_pair(begins, ends);
-      if (t + 1 < t1) {
-        pair0 += at.tiles;
-        at.next_pair<KT>(a);
-        begin_pair();
-        begins = true;
-      }
+    const bool ends = at.tile + 1 == at.tiles, stop = at.unit + 1 + (ends ? kPagedPairUnits : 0) >= t1;
+    if (ends || stop) end_pair(begins, ends);
+    if (stop) break;
+    ++at.tile;
+    ++at.unit;
+    if (ends) {
+      at.next_pair<KT>(a);
+      begin_pair();
+      begins = true;
     }
   }
 }
 
-// Joins the partials of the pairs that several warps shared: one warp per query row, or, when a row has more than 32
-// partials, the block's eight warps one row after the other.
+// Joins the partials of the pairs that several warps shared.  `per_row` warps (1, 2, 4 or 8) take a query row: a lane
+// reads the weight of one partial, all lanes its columns.
 template <int D>
-__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedArgs a, int rm) {
-  constexpr int V = D / 32;                        // columns of a lane
+__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedArgs a, int rm, int per_row) {
+  constexpr int V = D / 32;                        // columns of a lane: V lane .. V lane + V - 1
   __shared__ float so[8][D];
   __shared__ float2 sml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rows = static_cast<long long>(a.B) * a.H * a.N;
-  const long long row0 = static_cast<long long>(blockIdx.x) * 8;
-
-  struct Row { int b, hq, i, worker, more; long long first; };
-  auto find = [&](long long row) {
-    Row r;
-    r.i = static_cast<int>(row % a.N);
-    r.hq = static_cast<int>(row / a.N % a.H);
-    r.b = static_cast<int>(row / a.N / a.H);
-    const int h = r.hq / a.group, rr = (r.hq - h * a.group) * a.N + r.i, rt = rr / rm;
-    const int2 mt = a.meta[(static_cast<long long>(rt) * a.B + r.b) * a.H_kv + h];
-    r.worker = mt.x;
-    r.more = mt.y;
-    r.first = (static_cast<long long>(rt) * a.workers + mt.x) * 2 * a.part_rows + rr - rt * rm;
-    return r;
-  };
-  // partial j of a row: the first lies in slot 1 of its worker, the others in slot 0 of the workers behind it
-  auto place = [&](const Row& r, int j) {
-    return r.first + (2LL * j + (j == 0 ? 1 : 0)) * a.part_rows;
-  };
+  const unsigned rows = static_cast<unsigned>(a.B) * a.H * a.N;
+  const unsigned row = blockIdx.x * (8u / per_row) + warp / per_row;
+  const int sub = warp % per_row;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float acc[V];
-  float m, l;
-  auto gather = [&](const Row& r, int from, int step) {
-    m = -INFINITY;
-    l = 0.f;
+  float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    for (int j = from; j <= r.more; j += step) m = fmaxf(m, a.part_ml[place(r, j)].x);
-    const float nb = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-    for (int j = from; j <= r.more; j += step) {
-      const long long p = place(r, j);
-      const float2 ml = a.part_ml[p];
-      const float w = exp2f(ml.x - nb);
-      l = fmaf(w, ml.y, l);
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  int more = 0, b = 0, hq = 0, i = 0;
+  if (row < rows) {
+    i = static_cast<int>(row % a.N);
+    const unsigned bh = row / a.N;
+    hq = static_cast<int>(bh % a.H);
+    b = static_cast<int>(bh / a.H);
+    const int h = hq / a.group, rr = (hq - h * a.group) * a.N + i, rt = rr / rm;
+    const int2 mt = a.meta[(static_cast<long long>(rt) * a.B + b) * a.H_kv + h];
+    more = mt.y;
+    // partial j of the row: the first lies in slot 1 of its worker, the others in slot 0 of the workers behind it
+    const long long first = (static_cast<long long>(rt) * a.workers + mt.x) * 2 * a.part_rows + rr - rt * rm;
+    for (int j0 = 0; more > 0 && j0 <= more; j0 += 32 * per_row) {
+      const int mine = j0 + sub + lane * per_row;  // this lane's partial
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (mine <= more) ml = a.part_ml[first + (2LL * mine + (mine == 0 ? 1 : 0)) * a.part_rows];
+      float top = ml.x;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, a.part_o[p * D + lane + 32 * e], acc[e]);
-    }
-  };
-  auto put = [&](const Row& r) {
-    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-    __nv_bfloat16* o = a.o + row_offset(a.so, r.b, r.hq, r.i);
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mn = fmaxf(m, top), nb = mn == -INFINITY ? 0.f : mn;
+      const float old = exp2f(m - nb), w = mine <= more ? exp2f(ml.x - nb) : 0.f;
+      float sum = w * ml.y;
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
-    if (lane == 0)
-      a.lse[(static_cast<long long>(r.b) * a.H + r.hq) * a.N + r.i] =
-          l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-  };
-  constexpr int kAlone = 32;
-  if (row0 + warp < rows) {
-    const Row r = find(row0 + warp);
-    if (r.more > 0 && r.more < kAlone) {
-      gather(r, 0, 1);
-      put(r);
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = l * old + sum;
+      m = mn;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] *= old;
+      const int left = more - j0 - sub, cnt = left < 0 ? 0 : min(32, left / per_row + 1);
+#pragma unroll 8
+      for (int j = 0; j < cnt; ++j) {
+        const int p = j0 + sub + j * per_row;
+        const float f = __shfl_sync(0xffffffffu, w, j);
+        const float* src = a.part_o + (first + (2LL * p + (p == 0 ? 1 : 0)) * a.part_rows) * D + V * lane;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(src + e);
+          acc[e] = fmaf(f, x.x, acc[e]);
+          acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
+        }
+      }
     }
   }
-  for (int x = 0; x < 8 && row0 + x < rows; ++x) {
-    const Row r = find(row0 + x);                  // the same for every thread
-    if (r.more < kAlone) continue;
-    gather(r, warp, 8);
+  if (per_row > 1) {                               // the row's warps in order: results do not depend on timing
 #pragma unroll
-    for (int e = 0; e < V; ++e) so[warp][lane + 32 * e] = acc[e];
+    for (int e = 0; e < V; ++e) so[warp][V * lane + e] = acc[e];
     if (lane == 0) sml[warp] = make_float2(m, l);
     __syncthreads();
-    if (warp == 0) {
-      float top = -INFINITY;
-      for (int w = 0; w < 8; ++w) top = fmaxf(top, sml[w].x);
-      const float nb = top == -INFINITY ? 0.f : top;
-      m = top;
-      l = 0.f;
+    if (sub != 0) return;
+    float top = m;
+    for (int w = 1; w < per_row; ++w) top = fmaxf(top, sml[warp + w].x);
+    const float nb = top == -INFINITY ? 0.f : top, own = exp2f(m - nb);
+    m = top;
+    l *= own;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = 0.f;
-      for (int w = 0; w < 8; ++w) {
-        const float f = exp2f(sml[w].x - nb);
-        l = fmaf(f, sml[w].y, l);
+    for (int e = 0; e < V; ++e) acc[e] *= own;
+    for (int w = 1; w < per_row; ++w) {
+      const float f = exp2f(sml[warp + w].x - nb);
+      l = fmaf(f, sml[warp + w].y, l);
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(f, so[w][lane + 32 * e], acc[e]);
-      }
-      put(r);
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, so[warp + w][V * lane + e], acc[e]);
     }
-    __syncthreads();
   }
+  if (more == 0) return;                           // written by the warp that had the whole pair
+  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+  __nv_bfloat16* o = a.o + row_offset(a.so, b, hq, i) + V * lane;
+#pragma unroll
+  for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace fa

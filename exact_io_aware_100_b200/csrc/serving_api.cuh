@@ -83,7 +83,7 @@ fa_status check_decode(const fa_paged_layout& L) {
 
 // How a decode call is cut up, and where its workspace's parts lie.
 struct PagedPlan {
-  int rm, row_tiles, workers, part_rows;
+  int rm, row_tiles, workers, part_rows, min_units;
   size_t o_bytes, ml_bytes, meta_bytes;
   size_t bytes() const { return o_bytes + ml_bytes + meta_bytes; }
 };
@@ -93,10 +93,12 @@ PagedPlan paged_plan(const fa_paged_layout& L) {
   p.rm = paged_row_tile(L.d, rows);
   p.row_tiles = (rows + p.rm - 1) / p.rm;
   p.part_rows = rows < p.rm ? rows : p.rm;
-  // no more warps than the longest sequences that the table can hold give work to
+  // A range's partial (4 d bytes a row, written and read) should cost a quarter of its keys (4 d bytes each) at most
   const int kt = L.d == 64 ? 32 : 16;
-  const long long tiles = (1LL * L.max_pages * L.page_size + kt - 1) / kt * L.B * L.H_kv;
-  const long long ctas = (tiles + 4 * kPagedMinTiles - 1) / (4 * kPagedMinTiles);
+  p.min_units = std::max(kPagedMinUnits, 8 * p.part_rows / kt);
+  // no more warps than the longest sequences that the table can hold give work to
+  const long long units = ((1LL * L.max_pages * L.page_size + kt - 1) / kt + kPagedPairUnits) * L.B * L.H_kv;
+  const long long ctas = (units + 4 * p.min_units - 1) / (4 * p.min_units);
   p.workers = paged_workers(L.d, p.row_tiles);
   if (ctas < p.workers / 4) p.workers = static_cast<int>(ctas) * 4;
   const size_t parts = 2 * static_cast<size_t>(p.row_tiles) * p.workers * p.part_rows;
@@ -116,8 +118,19 @@ fa_status launch_paged(const PagedArgs& a, bool* attr, cudaStream_t s) {
     *attr = true;
   }
   fa_paged_decode_kernel<D, RM><<<dim3(a.workers / C::WARPS, a.row_tiles), C::THREADS, C::SMEM, s>>>(a);
+  // the merge: 8, 4, 2 or 1 warps to a row, as many as the GPU holds at once; launched while the first kernel runs
   const long long rows = 1LL * a.B * a.H * a.N;
-  fa_paged_merge_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a, RM);
+  const int per_row = rows <= kPagedSms * 8 ? 8 : rows <= kPagedSms * 16 ? 4 : rows <= kPagedSms * 32 ? 2 : 1;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows * per_row + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D>, a, static_cast<int>(RM), per_row) != cudaSuccess) return FA_ERR_CUDA;
   return launched();
 }
 
@@ -317,6 +330,7 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   a.workers = plan.workers;
   a.row_tiles = plan.row_tiles;
   a.part_rows = plan.part_rows;
+  a.min_units = plan.min_units;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + plan.o_bytes);

@@ -137,37 +137,34 @@ def fa_pages_copy(k_pages, v_pages, copies, layout: FaPagedLayout, stream=None) 
 
 
 # ----------------------------------------------------------------- where a call runs
-class _Launch:
-    """Makes the tensors' device (and ``stream``, if given) current for a call; checks that they share one device.
-    With a stream of the caller's the tensors are recorded as in use on it."""
+class _Here:
+    """The tensors' device is the current one and its current stream is meant: nothing to set up."""
+    __slots__ = ()
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+class _There:
+    """Makes the tensors' device and ``stream`` (if given) current for a call.  Tensors used on a stream of the caller's
+    are recorded as in use there."""
     __slots__ = ("guards", "tensors", "stream")
 
-    def __init__(self, stream, *tensors):
+    def __init__(self, stream, device, tensors):
         import torch
-        device = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("expected a CUDA tensor: the library reads and writes device memory only")
-            index = t.get_device()
-            if device is None:
-                device = index
-            elif index != device:
-                raise ValueError(f"tensors on different devices: cuda:{device} and cuda:{index}")
-        self.guards, self.tensors, self.stream = (), (), None
-        if device != torch.cuda.current_device():
-            self.guards = (torch.cuda.device(device),)
+        self.guards = (torch.cuda.device(device),)
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
             self.guards += (torch.cuda.stream(stream),)
-            self.tensors, self.stream = tensors, stream
+        self.tensors, self.stream = tensors, stream
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return self
 
     def __exit__(self, *exc):
         if self.stream is not None and exc[0] is None:
@@ -180,9 +177,30 @@ class _Launch:
             g.__exit__(*exc)
 
 
+_HERE = _Here()
+
+
+def _launch(stream, *tensors):
+    """Where a call on these tensors runs, as a context; checks that they share one CUDA device."""
+    import torch
+    device = None
+    for t in tensors:
+        if t is not None:
+            index = t.get_device()
+            if index != device:
+                if index < 0:
+                    raise ValueError("expected a CUDA tensor: the library reads and writes device memory only")
+                if device is not None:
+                    raise ValueError(f"tensors on different devices: cuda:{device} and cuda:{index}")
+                device = index
+    if stream is None and device == torch.cuda.current_device():
+        return _HERE
+    return _There(stream, device, tensors)
+
+
 def _int32(t, name: str, dims: int):
     import torch
-    if t.dtype != torch.int32 or t.dim() != dims or (t.numel() > 1 and t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dtype != torch.int32 or t.dim() != dims or (t.stride(-1) != 1 and t.numel() > 1 and t.shape[-1] > 1):
         raise ValueError(f"{name}: expected a {dims}-D int32 tensor, contiguous in its last axis")
 
 
@@ -190,7 +208,7 @@ def _rows(t, name: str, dims, dtypes):
     """Checks [B, heads, rows, d] (4-D) or packed [rows, heads, d] (3-D); d contiguous."""
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() not in dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dim() not in dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name}: expected [B, heads, rows, d]" + (" or packed [rows, heads, d]" if 3 in dims else "") +
                          " with contiguous d")
 
@@ -280,7 +298,7 @@ def _rotary(q, k, freqs, positions, interleaved, magnitude, out, inverse, stream
         if positions.shape[-1] != N or (positions.dim() == 2 and positions.shape[0] != B):
             raise ValueError("positions: expected one per row ([rows] or [B, rows])")
         pos_batch = positions.stride(0) if positions.dim() == 2 else 0
-    with _Launch(stream, q, k, freqs, positions, *(out or ())):
+    with _launch(stream, q, k, freqs, positions, *(out or ())):
         if out is None:
             q_out, k_out = torch.empty_like(q), None if k is None else torch.empty_like(k)
         else:
@@ -353,7 +371,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q=None, freqs=Non
         if q.shape[0] != k.shape[0] or q.shape[-1] != d or (not packed and q.shape[2] != k.shape[2]):
             raise ValueError("q and k: batch, rows and d must agree")
     r = 0 if freqs is None else _freqs(freqs)
-    with _Launch(stream, q, k, v, k_pages, v_pages, page_table, seq_lens, freqs, cu_seqlens, out):
+    with _launch(stream, q, k, v, k_pages, v_pages, page_table, seq_lens, freqs, cu_seqlens, out):
         if out is None:
             out = None if q is None else torch.empty_like(q)
         elif q is None or out.shape != q.shape or out.dtype != q.dtype or (d > 1 and out.stride(-1) != 1):
@@ -377,9 +395,9 @@ def paged_decode(q, k_pages, v_pages, page_table, seq_lens, causal: bool = True,
     if dq != d:
         raise ValueError("q and the cache: d must agree")
     M = _table(page_table, seq_lens, B)
-    with _Launch(stream, q, k_pages, v_pages, page_table, seq_lens, workspace):
+    with _launch(stream, q, k_pages, v_pages, page_table, seq_lens, workspace):
         o = torch.empty_like(q)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, H, N), dtype=torch.float32)
         layout = FaPagedLayout(B, H, H_kv, d, N, P, page, M, page_table.stride(0), *_st(q), *_st(o), 0, 0, 0, 0, 0, 0,
                                *k_pages.stride()[:3], *v_pages.stride()[:3], None, 0, 0, 0)
         if workspace is None:
@@ -410,7 +428,7 @@ def pages_extend(page_table, seq_lens, refcounts, page_size: int, seqs, tokens, 
     that is not FA_OK changed nothing."""
     import torch
     layout = _pages_state(page_table, seq_lens, refcounts, page_size, ("seqs", seqs), ("tokens", tokens))
-    with _Launch(stream, page_table, seq_lens, refcounts, seqs, tokens, workspace):
+    with _launch(stream, page_table, seq_lens, refcounts, seqs, tokens, workspace):
         status = torch.empty_like(seqs)
         fa_pages_extend(page_table, seq_lens, refcounts, layout, seqs, tokens, status,
                         _pages_workspace(layout, seqs.numel(), workspace, seqs.device))
@@ -423,7 +441,7 @@ def pages_fork(page_table, seq_lens, refcounts, page_size: int, src, dst, stream
     brings the contents over, in each layer's cache."""
     import torch
     layout = _pages_state(page_table, seq_lens, refcounts, page_size, ("src", src), ("dst", dst))
-    with _Launch(stream, page_table, seq_lens, refcounts, src, dst, workspace):
+    with _launch(stream, page_table, seq_lens, refcounts, src, dst, workspace):
         status = torch.empty_like(src)
         copies = torch.empty((src.numel(), 3), dtype=torch.int32, device=src.device)
         fa_pages_fork(page_table, seq_lens, refcounts, layout, src, dst, copies, status,
@@ -434,7 +452,7 @@ def pages_fork(page_table, seq_lens, refcounts, page_size: int, src, dst, stream
 def pages_free(page_table, seq_lens, refcounts, page_size: int, seqs, stream=None) -> None:
     """Sequences ``seqs`` (int32 [n]) become empty; their pages are free once no other sequence holds them."""
     layout = _pages_state(page_table, seq_lens, refcounts, page_size, ("seqs", seqs))
-    with _Launch(stream, page_table, seq_lens, refcounts, seqs):
+    with _launch(stream, page_table, seq_lens, refcounts, seqs):
         fa_pages_free(page_table, seq_lens, refcounts, layout, seqs)
 
 
@@ -442,7 +460,7 @@ def pages_compact(page_table, seq_lens, refcounts, page_size: int, stream=None, 
     """Moves the pages in use to the lowest numbers.  Returns copies int32 [pages // 2, 3] for ``pages_copy``."""
     import torch
     layout = _pages_state(page_table, seq_lens, refcounts, page_size)
-    with _Launch(stream, page_table, seq_lens, refcounts, workspace):
+    with _launch(stream, page_table, seq_lens, refcounts, workspace):
         copies = torch.empty((refcounts.numel() // 2, 3), dtype=torch.int32, device=refcounts.device)
         fa_pages_compact(page_table, seq_lens, refcounts, layout, copies,
                          _pages_workspace(layout, 0, workspace, refcounts.device))
@@ -455,7 +473,7 @@ def pages_copy(k_pages, v_pages, copies, stream=None) -> None:
     _int32(copies, "copies", 2)
     if copies.shape[1] != 3 or not copies.is_contiguous():
         raise ValueError("copies: expected a contiguous [n, 3] tensor")
-    with _Launch(stream, k_pages, v_pages, copies):
+    with _launch(stream, k_pages, v_pages, copies):
         layout = FaPagedLayout(1, 0, H_kv, d, 0, P, page, 0, 0, *(0,) * 12, *k_pages.stride()[:3],
                                *v_pages.stride()[:3], None, 0, 0, 0)
         fa_pages_copy(k_pages, v_pages, copies, layout)
