@@ -21,9 +21,10 @@
 //  * the products are warp-level matrix instructions (16 rows x 8 columns x 16): rows
 //    are few, and the tcgen05 tiles start at 64 rows.  S = Q K^T gives its accumulators
 //    in the layout that P V wants its left operand in, so P stays in registers;
-//  * P is split in two bf16 parts, hi + lo (16 bits of mantissa): with at most 8 rows
-//    the lo parts ride in the 8 unused rows of the same instruction, otherwise they
-//    take a second one.  Everything else is 32-bit; O is rounded once.
+//  * P is rounded to bf16 for the second product; with at most 8 rows its remainder rides
+//    in the 8 unused rows of the same instruction, which makes it 16 bits of mantissa.
+//    (With more rows the remainder would take a second instruction.)  Everything else
+//    is 32-bit; O is rounded once.
 //  * O is rescaled only when a row's maximum grows by more than 2^8.
 #pragma once
 
@@ -230,40 +231,38 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         look_up(want + 32);
       }
       constexpr int CH = D / 8, RPI = 32 / CH;     // 16-byte chunks of a key; keys per warp copy
-      const uint32_t st = ring + load_stage * C::STAGE;
       const int ch = lane % CH, r0 = lane / CH;
-#pragma unroll
+      uint32_t st = ring + load_stage * C::STAGE + r0 * C::PITCH;
+#pragma unroll 1
       for (int u = 0; u < KT / 8; ++u) {
-        const int p = __shfl_sync(0xffffffffu, pg, (g - g0) + u), row = __shfl_sync(0xffffffffu, row_in, (g - g0) + u);
-        const __nv_bfloat16* k = a.kp + (p < 0 ? 0 : row_offset(a.skp, p, in.h, row + r0) + ch * 8);
-        const __nv_bfloat16* v = a.vp + (p < 0 ? 0 : row_offset(a.svp, p, in.h, row + r0) + ch * 8);
-        const int left = p < 0 ? 0 : in.len - (g + u) * 8;     // keys of this group that exist
-        const long long ks = p < 0 ? 0 : a.skp.r * RPI, vs = p < 0 ? 0 : a.svp.r * RPI;
+        const int p = __shfl_sync(0xffffffffu, pg, (g - g0) + u), row = __shfl_sync(0xffffffffu, row_in, (g - g0) + u) + r0;
+        const int left = p < 0 ? 0 : in.len - (g + u) * 8 - r0;   // this lane's keys r < left exist; others: zeros
+        const __nv_bfloat16* k = a.kp + row_offset(a.skp, max(p, 0), in.h, row) + ch * 8;
+        const __nv_bfloat16* v = a.vp + row_offset(a.svp, max(p, 0), in.h, row) + ch * 8;
 #pragma unroll
         for (int r = 0; r < 8; r += RPI) {
-          const int key = u * 8 + r + r0;
-          const bool real = r + r0 < left;
-          const uint32_t dst = st + key * C::PITCH + ((ch ^ (key & 7)) << 4);
-          copy16(dst, real ? k : a.kp, real);
-          copy16(dst + C::TILE, real ? v : a.vp, real);
-          k += ks;
-          v += vs;
+          const uint32_t dst = st + r * C::PITCH + ((ch ^ (r + r0)) << 4);
+          copy16(dst, k, r < left);
+          copy16(dst + C::TILE, v, r < left);
+          k += RPI * a.skp.r;
+          v += RPI * a.svp.r;
         }
+        st += 8 * C::PITCH;
       }
       ++in.unit;
-      if (++in.tile == in.tiles && in.unit + kPagedPairUnits < t1) {
-        const int b = in.b;
-        in.next_pair<KT>(a);
-        if (in.b != b) g0 = -1;
-      } else if (in.tile == in.tiles) {
-        in.unit = t1;
+      if (++in.tile == in.tiles) {
+        if (in.unit + kPagedPairUnits < t1) {
+          const int b = in.b;
+          in.next_pair<KT>(a);
+          if (in.b != b) g0 = -1;
+        } else {
+          in.unit = t1;
+        }
       }
       load_stage = load_stage + 1 == C::STAGES ? 0 : load_stage + 1;
     }
     copy_commit();
   };
-#pragma unroll
-  for (int s = 0; s < C::STAGES - 1; ++s) load_tile();
 
   // ---- a pair's rows: this thread's rows of the 16-row tiles are lane / 4 and (unless HALF) lane / 4 + 8
   const int quad = lane & 3;
@@ -273,30 +272,51 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   float m[MT][RW], l[MT][RW];
   int lim[MT][RW];                                 // last key the row sees
   auto row_of = [&](int mt, int w) { return rt * RM + mt * 16 + w * 8 + (lane >> 2); };
+  // Q goes through the stage that is loaded next, rows without a query as zeros.
   auto begin_pair = [&]() {
+    const uint32_t st = ring + load_stage * C::STAGE;
+#pragma unroll 1
+    for (int e = lane; e < RM * (D / 8); e += 32) {
+      const int rr = e / (D / 8), ch = e % (D / 8), r = rt * RM + rr, g = r / a.N, i = r - g * a.N;
+      copy16(st + rr * C::PITCH + ((ch ^ (rr & 7)) << 4),
+             a.q + (r < a.rows ? row_offset(a.sq, at.b, at.h * a.group + g, i) + ch * 8 : 0), r < a.rows);
+    }
+    copy_commit();
+    copy_wait<0>();
+    __syncwarp();
+    const int row = (lane & 7) + (C::HALF ? 0 : ((lane >> 3) & 1) * 8), hi = C::HALF ? lane >> 3 : lane >> 4;
+    const uint32_t qa = st + row * C::PITCH + ((hi ^ (row & 7)) << 4);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+      if constexpr (C::HALF) {                     // two k-steps at a time: chunks 4 x .. 4 x + 3
+#pragma unroll
+        for (int k = 0; k < D / 16; k += 2) {
+          uint32_t w[4];
+          ldsm4(qa ^ (32 * k), w);
+          qf[0][k][0] = w[0];
+          qf[0][k][1] = w[1];
+          qf[0][k + 1][0] = w[2];
+          qf[0][k + 1][1] = w[3];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) ldsm4((qa ^ (32 * k)) + mt * 16 * C::PITCH, qf[mt][k]);
+      }
 #pragma unroll
       for (int w = 0; w < RW; ++w) {
-        const int r = row_of(mt, w), g = r / a.N, i = r - g * a.N;
-        lim[mt][w] = a.causal ? at.len - a.N + i : at.len - 1;
+        lim[mt][w] = a.causal ? at.len - a.N + row_of(mt, w) % a.N : at.len - 1;
         m[mt][w] = -INFINITY;
         l[mt][w] = 0.f;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            a.q + (r < a.rows ? row_offset(a.sq, at.b, at.h * a.group + g, i) : 0)) + quad;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          qf[mt][k][w] = r < a.rows ? __ldg(src + 8 * k) : 0u;
-          qf[mt][k][RW + w] = r < a.rows ? __ldg(src + 8 * k + 4) : 0u;
-        }
       }
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.f;
     }
+    __syncwarp();                                  // everyone has its Q: the stage is free
   };
   auto end_pair = [&](bool begins, bool ends) {    // of the pair's tiles this warp had the first, the last
+    const bool whole = begins && ends;
     const long long slot = ((static_cast<long long>(rt) * a.workers + worker) * 2 + (begins ? 1 : 0)) * a.part_rows;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -309,28 +329,23 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         if (r >= a.rows) continue;
         const int g = r / a.N, i = r - g * a.N, hq = at.h * a.group + g;
         const float top = m[mt][w] == -INFINITY ? -INFINITY : m[mt][w] * c2;
-        if (begins && ends) {
-          const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
-          __nv_bfloat16* o = a.o + row_offset(a.so, at.b, hq, i) + 2 * quad;
+        const float f = !whole ? 1.0f : sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+        const long long pr = slot + r - rt * RM;
+        char* o = whole ? reinterpret_cast<char*>(a.o + row_offset(a.so, at.b, hq, i) + 2 * quad)
+                        : reinterpret_cast<char*>(a.part_o + pr * D + 2 * quad);
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            const float x = C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w];
-            const float y = C::HALF ? acc[mt][n][1] + acc[mt][n][3] : acc[mt][n][2 * w + 1];
-            *reinterpret_cast<uint32_t*>(o + 8 * n) = pack_bf16x2(x * inv, y * inv);
-          }
-          if (quad == 0)
+        for (int n = 0; n < D / 8; ++n) {
+          const float x = f * (C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w]);
+          const float y = f * (C::HALF ? acc[mt][n][1] + acc[mt][n][3] : acc[mt][n][2 * w + 1]);
+          if (whole) *reinterpret_cast<uint32_t*>(o + 16 * n) = pack_bf16x2(x, y);
+          else *reinterpret_cast<float2*>(o + 32 * n) = make_float2(x, y);
+        }
+        if (quad == 0) {
+          if (whole)
             a.lse[(static_cast<long long>(at.b) * a.H + hq) * a.N + i] =
                 sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-        } else {
-          const long long pr = slot + r - rt * RM;
-          float* o = a.part_o + pr * D + 2 * quad;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            const float x = C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w];
-            const float y = C::HALF ? acc[mt][n][1] + acc[mt][n][3] : acc[mt][n][2 * w + 1];
-            *reinterpret_cast<float2*>(o + 8 * n) = make_float2(x, y);
-          }
-          if (quad == 0) a.part_ml[pr] = make_float2(top, sum);
+          else
+            a.part_ml[pr] = make_float2(top, sum);
         }
       }
     if (begins && lane == 0) {
@@ -339,13 +354,22 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     }
   };
 
-  begin_pair();
-  bool begins = at.tile == 0;
+  // One copy of every step in the code: a launch runs each of them a few times only, and what it costs then is fetching
+  // the instructions (two more copies of load_tile and one of begin_pair took the shortest calls from 7 to 12-30 us).
+  bool fresh = true, begins = at.tile == 0;
   int stage = 0;
-  while (true) {
-    copy_wait<C::STAGES - 2>();
-    __syncwarp();                                  // everyone's copies of this tile; everyone is done with the last one
+#pragma unroll 1
+  for (int ahead = C::STAGES - 1;;) {              // tiles to load before the first is used
+    if (ahead == 0) {
+      copy_wait<C::STAGES - 2>();
+      __syncwarp();                                // everyone's copies of this tile; everyone is done with the last one
+      if (fresh) begin_pair();
+    }
     load_tile();
+    if (ahead > 0) {
+      --ahead;
+      continue;
+    }
     const uint32_t ks = ring + stage * C::STAGE, vs = ks + C::TILE;
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
     // ---- S = Q K^T
@@ -358,12 +382,13 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
     {
       const int row = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+      const uint32_t ka = ks + row * C::PITCH + ((hi ^ (row & 7)) << 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t kf[4];
-          ldsm4(ks + (row + 8 * n) * C::PITCH + (((2 * k + hi) ^ (row & 7)) << 4), kf);
+          ldsm4((ka ^ (32 * k)) + 8 * n * C::PITCH, kf);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const uint32_t a0 = qf[mt][k][0], a1 = C::HALF ? 0u : qf[mt][k][1], a2 = qf[mt][k][RW],
@@ -415,7 +440,7 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
             l[mt][w] += p;
           }
       }
-    if (__any_sync(0xffffffffu, grew)) {
+    if (!fresh && __any_sync(0xffffffffu, grew)) { // on a pair's first tile there is nothing to rescale
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -423,35 +448,34 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[mt][n][e] *= alpha[mt][C::HALF ? 0 : e >> 1];
     }
+    fresh = false;
     // ---- O += P V
 #pragma unroll
     for (int kk = 0; kk < NT / 2; ++kk) {
-      uint32_t hi[MT][2 * RW], lo[MT][2 * RW];     // keys 0 .. 7 of the 16 (rows, rows + 8), then keys 8 .. 15
+      uint32_t p[MT][4];                           // keys 0 .. 7 of the 16 (rows, rows + 8), then keys 8 .. 15
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int x = 0; x < 2 * RW; ++x) {
-          const float* p = &s[mt][2 * kk + x / RW][2 * (x % RW)];
-          hi[mt][x] = pack_bf16x2(p[0], p[1]);
-          const float2 h = bf16x2_to_float2(hi[mt][x]);
-          lo[mt][x] = pack_bf16x2(p[0] - h.x, p[1] - h.y);
+        for (int x = 0; x < 2; ++x) {
+          const float* y = s[mt][2 * kk + x];
+          p[mt][2 * x] = pack_bf16x2(y[0], y[1]);
+          if constexpr (C::HALF) {
+            const float2 h = bf16x2_to_float2(p[mt][2 * x]);
+            p[mt][2 * x + 1] = pack_bf16x2(y[0] - h.x, y[1] - h.y);
+          } else {
+            p[mt][2 * x + 1] = pack_bf16x2(y[2], y[3]);
+          }
         }
-      const int row = 16 * kk + (lane & 15), c0 = lane >> 4;
+      const int row = lane & 15;
+      const uint32_t va = vs + (16 * kk + row) * C::PITCH + (((lane >> 4) ^ (row & 7)) << 4);
 #pragma unroll
       for (int n = 0; n < D / 8; n += 2) {
         uint32_t vf[4];
-        ldsm4_t(vs + row * C::PITCH + (((n + c0) ^ (row & 7)) << 4), vf);
+        ldsm4_t(va ^ (16 * n), vf);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          if constexpr (C::HALF) {
-            mma_bf16(acc[mt][n], hi[mt][0], lo[mt][0], hi[mt][1], lo[mt][1], vf[0], vf[1]);
-            mma_bf16(acc[mt][n + 1], hi[mt][0], lo[mt][0], hi[mt][1], lo[mt][1], vf[2], vf[3]);
-          } else {
-            mma_bf16(acc[mt][n], hi[mt][0], hi[mt][1], hi[mt][2], hi[mt][3], vf[0], vf[1]);
-            mma_bf16(acc[mt][n + 1], hi[mt][0], hi[mt][1], hi[mt][2], hi[mt][3], vf[2], vf[3]);
-            mma_bf16(acc[mt][n], lo[mt][0], lo[mt][1], lo[mt][2], lo[mt][3], vf[0], vf[1]);
-            mma_bf16(acc[mt][n + 1], lo[mt][0], lo[mt][1], lo[mt][2], lo[mt][3], vf[2], vf[3]);
-          }
+          mma_bf16(acc[mt][n], p[mt][0], p[mt][1], p[mt][2], p[mt][3], vf[0], vf[1]);
+          mma_bf16(acc[mt][n + 1], p[mt][0], p[mt][1], p[mt][2], p[mt][3], vf[2], vf[3]);
         }
       }
     }
@@ -462,8 +486,7 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     ++at.unit;
     if (ends) {
       at.next_pair<KT>(a);
-      begin_pair();
-      begins = true;
+      fresh = begins = true;
     }
   }
 }
