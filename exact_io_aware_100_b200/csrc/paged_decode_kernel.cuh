@@ -12,12 +12,14 @@
 //    pair, whole pairs, and the beginning of another; whole pairs are written out,
 //    the cut ones leave (max, sum, O) partials that the merge kernel joins.  The
 //    lengths are read on the device: a captured call follows them;
-//  * a warp fills its own ring of tiles with 16-byte asynchronous copies, across the
-//    ends of pairs, and waits for nobody: no block barrier in the loop.  Beginning and
-//    ending a pair (its rows' loads, its outputs) counts as kPagedPairUnits tiles.  A tile is
-//    gathered 8 keys at a time (8 divides the page size), and the page numbers of 256
-//    keys are read ahead.  Keys behind the sequence's end are filled with zeros in
-//    shared memory, so what the pages hold there does not matter;
+//  * a warp fills its own ring of tiles by TMA, across the ends of pairs, and waits for
+//    nobody: no block barrier in the loop.  Beginning and ending a pair (its rows'
+//    loads, its outputs) counts as kPagedPairUnits tiles.  A box is 8, 16 or 32 keys of
+//    all d columns, the most that divides tile and page; the page numbers of 256 keys
+//    are read ahead, and a number that names no page loads zeros (it lies outside the
+//    tensor map).  Values behind a sequence's end are zeroed in shared memory, and
+//    scores there masked, so what the pages hold there does not matter.  (Gathering
+//    with 16-byte asynchronous copies took 150-250 instructions per tile more.);
 //  * the products are warp-level matrix instructions (16 rows x 8 columns x 16): rows
 //    are few, and the tcgen05 tiles start at 64 rows.  S = Q K^T gives its accumulators
 //    in the layout that P V wants its left operand in, so P stays in registers;
@@ -50,6 +52,8 @@ struct PagedArgs {
   int row_tiles;
   int part_rows;                   // rows of a partial
   float* part_o;                   // [row tile][worker][2][part_rows][D]
+  unsigned long long wait_limit_ns;
+  int box;                         // keys of a TMA box: 8, 16 or 32
   float2* part_ml;                 // [row tile][worker][2][part_rows] maximum (log2 units) and sum
   int2* meta;                      // [row tile][B][H_kv] worker where the pair begins, workers it goes on into
   uint32_t* status;
@@ -75,11 +79,11 @@ struct PagedCfg {
   static constexpr int NT = KT / 8;
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
   static constexpr int STAGES = 3;
-  static constexpr int PITCH = 2 * D;            // bytes of a key in shared memory
-  static constexpr int TILE = KT * PITCH;
+  static constexpr int PITCH = 2 * D;            // bytes of a key, or of a query
+  static constexpr int TILE = KT * PITCH;        // [box][64 columns][key][128 bytes], 128-byte swizzle
   static constexpr int STAGE = 2 * TILE;         // K, then V
   static constexpr int RING = STAGES * STAGE;
-  static constexpr int SMEM = WARPS * RING;
+  static constexpr int SMEM = WARPS * RING + 1024;   // and what aligns it
   static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
 };
 constexpr int kPagedSms = 148;
@@ -108,6 +112,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
 }
 // 16 bytes to shared memory, or 16 zero bytes.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
@@ -140,15 +152,30 @@ struct PagedPlace {
 
 template <int D, int RM>
 __global__ void __launch_bounds__(128, (PagedCfg<D, RM>::CTAS))
-fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
+fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ PagedArgs a) {
   using C = PagedCfg<D, RM>;
   constexpr int KT = C::KT, NT = C::NT, MT = C::MT, RW = C::HALF ? 1 : 2;   // RW: rows of a thread in a 16-row tile
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ long long before[C::THREADS + 1];
   __shared__ long long warp_sum[C::WARPS];
+  __shared__ uint64_t bars[C::WARPS * C::STAGES];  // a stage's bytes have arrived
+  __shared__ uint32_t abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int worker = blockIdx.x * C::WARPS + warp, rt = blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge kernel may come up, and waits for the end
+
+  const uint32_t bar0 = smem_u32(bars + warp * C::STAGES);
+  if (lane == 0) {
+    for (int st = 0; st < C::STAGES; ++st) mbar_init(bar0 + 8 * st, 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (tid == 0) abort_flag = 0u;                   // the barriers below come before every use
 
   // ---- the line, of one head: thread t sums the units of sequences t q .. t q + q - 1
   const int per_thread = (a.B + C::THREADS - 1) / C::THREADS;
@@ -230,24 +257,15 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         g0 = want;
         look_up(want + 32);
       }
-      constexpr int CH = D / 8, RPI = 32 / CH;     // 16-byte chunks of a key; keys per warp copy
-      const int ch = lane % CH, r0 = lane / CH;
-      uint32_t st = ring + load_stage * C::STAGE + r0 * C::PITCH;
+      const uint32_t st = ring + load_stage * C::STAGE, bar = bar0 + 8 * load_stage;
+      if (lane == 0) mbar_expect_tx(bar, C::STAGE);
 #pragma unroll 1
-      for (int u = 0; u < KT / 8; ++u) {
-        const int p = __shfl_sync(0xffffffffu, pg, (g - g0) + u), row = __shfl_sync(0xffffffffu, row_in, (g - g0) + u) + r0;
-        const int left = p < 0 ? 0 : in.len - (g + u) * 8 - r0;   // this lane's keys r < left exist; others: zeros
-        const __nv_bfloat16* k = a.kp + row_offset(a.skp, max(p, 0), in.h, row) + ch * 8;
-        const __nv_bfloat16* v = a.vp + row_offset(a.svp, max(p, 0), in.h, row) + ch * 8;
-#pragma unroll
-        for (int r = 0; r < 8; r += RPI) {
-          const uint32_t dst = st + r * C::PITCH + ((ch ^ (r + r0)) << 4);
-          copy16(dst, k, r < left);
-          copy16(dst + C::TILE, v, r < left);
-          k += RPI * a.skp.r;
-          v += RPI * a.svp.r;
+      for (int key = 0; key < KT; key += a.box) {
+        const int p = __shfl_sync(0xffffffffu, pg, (g - g0) + key / 8), row = __shfl_sync(0xffffffffu, row_in, (g - g0) + key / 8);
+        if (lane == 0) {
+          tma_load_5d(st + key * C::PITCH, &tm_k, bar, 0, row, 0, in.h, p);
+          tma_load_5d(st + key * C::PITCH + C::TILE, &tm_v, bar, 0, row, 0, in.h, p);
         }
-        st += 8 * C::PITCH;
       }
       ++in.unit;
       if (++in.tile == in.tiles) {
@@ -261,7 +279,6 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       }
       load_stage = load_stage + 1 == C::STAGES ? 0 : load_stage + 1;
     }
-    copy_commit();
   };
 
   // ---- a pair's rows: this thread's rows of the 16-row tiles are lane / 4 and (unless HALF) lane / 4 + 8
@@ -270,16 +287,21 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   uint32_t qf[MT][D / 16][C::HALF ? 2 : 4];
   float acc[MT][D / 8][4];
   float m[MT][RW], l[MT][RW];
-  int lim[MT][RW];                                 // last key the row sees
-  auto row_of = [&](int mt, int w) { return rt * RM + mt * 16 + w * 8 + (lane >> 2); };
+  // lane r holds where row r of the row tile lies behind its pair's first query head
+  const int my_row = rt * RM + lane, my_g = my_row / a.N, my_i = my_row - my_g * a.N;
+  const bool my_real = lane < RM && my_row < a.rows;
+  const long long q_row = my_real ? my_g * a.sq.h + my_i * a.sq.r : -1, o_row = my_g * a.so.h + my_i * a.so.r;
   // Q goes through the stage that is loaded next, rows without a query as zeros.
   auto begin_pair = [&]() {
     const uint32_t st = ring + load_stage * C::STAGE;
+    constexpr int CH = D / 8, RPI = 32 / CH;       // 16-byte chunks of a row; rows per warp copy
+    const int ch = lane % CH;
+    const __nv_bfloat16* q = a.q + at.b * a.sq.b + static_cast<long long>(at.h) * a.group * a.sq.h + ch * 8;
 #pragma unroll 1
-    for (int e = lane; e < RM * (D / 8); e += 32) {
-      const int rr = e / (D / 8), ch = e % (D / 8), r = rt * RM + rr, g = r / a.N, i = r - g * a.N;
-      copy16(st + rr * C::PITCH + ((ch ^ (rr & 7)) << 4),
-             a.q + (r < a.rows ? row_offset(a.sq, at.b, at.h * a.group + g, i) + ch * 8 : 0), r < a.rows);
+    for (int r = 0; r < RM; r += RPI) {
+      const int rr = r + lane / CH;
+      const long long off = __shfl_sync(0xffffffffu, q_row, rr);
+      copy16(st + rr * C::PITCH + ((ch ^ (rr & 7)) << 4), off < 0 ? a.q : q + off, off >= 0);
     }
     copy_commit();
     copy_wait<0>();
@@ -304,7 +326,6 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       }
 #pragma unroll
       for (int w = 0; w < RW; ++w) {
-        lim[mt][w] = a.causal ? at.len - a.N + row_of(mt, w) % a.N : at.len - 1;
         m[mt][w] = -INFINITY;
         l[mt][w] = 0.f;
       }
@@ -313,11 +334,14 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.f;
     }
-    __syncwarp();                                  // everyone has its Q: the stage is free
+    fence_proxy_async_smem();
+    __syncwarp();                                  // everyone has its Q: the stage is free for TMA
   };
   auto end_pair = [&](bool begins, bool ends) {    // of the pair's tiles this warp had the first, the last
     const bool whole = begins && ends;
     const long long slot = ((static_cast<long long>(rt) * a.workers + worker) * 2 + (begins ? 1 : 0)) * a.part_rows;
+    const long long head0 = static_cast<long long>(at.b) * a.H + at.h * a.group;
+    __nv_bfloat16* o = a.o + at.b * a.so.b + static_cast<long long>(at.h) * a.group * a.so.h + 2 * quad;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -325,27 +349,26 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         float sum = l[mt][w];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int r = row_of(mt, w);
-        if (r >= a.rows) continue;
-        const int g = r / a.N, i = r - g * a.N, hq = at.h * a.group + g;
-        const float top = m[mt][w] == -INFINITY ? -INFINITY : m[mt][w] * c2;
-        const float f = !whole ? 1.0f : sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
-        const long long pr = slot + r - rt * RM;
-        char* o = whole ? reinterpret_cast<char*>(a.o + row_offset(a.so, at.b, hq, i) + 2 * quad)
-                        : reinterpret_cast<char*>(a.part_o + pr * D + 2 * quad);
+        const int rr = mt * 16 + w * 8 + (lane >> 2);
+        const long long off = __shfl_sync(0xffffffffu, o_row, rr);
+        if (rt * RM + rr < a.rows) {
+          const float top = m[mt][w] == -INFINITY ? -INFINITY : m[mt][w] * c2;
+          const float f = !whole ? 1.0f : sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+          char* to = whole ? reinterpret_cast<char*>(o + off)
+                           : reinterpret_cast<char*>(a.part_o + (slot + rr) * D + 2 * quad);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          const float x = f * (C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w]);
-          const float y = f * (C::HALF ? acc[mt][n][1] + acc[mt][n][3] : acc[mt][n][2 * w + 1]);
-          if (whole) *reinterpret_cast<uint32_t*>(o + 16 * n) = pack_bf16x2(x, y);
-          else *reinterpret_cast<float2*>(o + 32 * n) = make_float2(x, y);
-        }
-        if (quad == 0) {
-          if (whole)
-            a.lse[(static_cast<long long>(at.b) * a.H + hq) * a.N + i] =
-                sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-          else
-            a.part_ml[pr] = make_float2(top, sum);
+          for (int n = 0; n < D / 8; ++n) {
+            const float x = f * (C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w]);
+            const float y = f * (C::HALF ? acc[mt][n][1] + acc[mt][n][3] : acc[mt][n][2 * w + 1]);
+            if (whole) *reinterpret_cast<uint32_t*>(to + 16 * n) = pack_bf16x2(x, y);
+            else *reinterpret_cast<float2*>(to + 32 * n) = make_float2(x, y);
+          }
+          if (quad == 0) {
+            if (whole)
+              a.lse[head0 * a.N + rt * RM + rr] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            else
+              a.part_ml[slot + rr] = make_float2(top, sum);
+          }
         }
       }
     if (begins && lane == 0) {
@@ -358,11 +381,24 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   // the instructions (two more copies of load_tile and one of begin_pair took the shortest calls from 7 to 12-30 us).
   bool fresh = true, begins = at.tile == 0;
   int stage = 0;
+  uint32_t phase = 0;                              // bit of each stage: parity of its next arrival
+  const WaitCtl ctl{&abort_flag, a.status, a.wait_limit_ns};
+  // where key `key` of a tile lies, and the bytes between its 64-column pieces
+  const int piece = a.box * 128;
+  auto key_at = [&](int key) { return D == 64 ? key * 128 : key / a.box * (a.box * C::PITCH) + key % a.box * 128; };
+  const int krow = (lane & 7) + ((lane >> 4) << 3), vrow = lane & 15;
+  const uint32_t k_lane = key_at(krow) + ((((lane >> 3) & 1) ^ (krow & 7)) << 4);
+  const uint32_t v_lane = C::TILE + key_at(vrow) + (((lane >> 4) ^ (vrow & 7)) << 4);
 #pragma unroll 1
   for (int ahead = C::STAGES - 1;;) {              // tiles to load before the first is used
     if (ahead == 0) {
-      copy_wait<C::STAGES - 2>();
-      __syncwarp();                                // everyone's copies of this tile; everyone is done with the last one
+      if (!mbar_wait_warp(bar0 + 8 * stage, (phase >> stage) & 1, ctl)) {   // (and everyone is done with the last tile)
+        // let the copies in flight land (bounded): every stage but the free one
+        if (lane == 0)
+          for (int st = 0; st < C::STAGES; ++st)
+            if (st != load_stage) mbar_wait_quiet(bar0 + 8 * st, (phase >> st) & 1, 200000000ull);
+        return;
+      }
       if (fresh) begin_pair();
     }
     load_tile();
@@ -370,7 +406,8 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       --ahead;
       continue;
     }
-    const uint32_t ks = ring + stage * C::STAGE, vs = ks + C::TILE;
+    const uint32_t ks = ring + stage * C::STAGE;
+    phase ^= 1u << stage;
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
     // ---- S = Q K^T
     float s[MT][NT][4];
@@ -381,14 +418,13 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
     {
-      const int row = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
-      const uint32_t ka = ks + row * C::PITCH + ((hi ^ (row & 7)) << 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
+        const uint32_t ka = (ks + k_lane + k / 4 * piece) ^ (32 * (k % 4));
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t kf[4];
-          ldsm4((ka ^ (32 * k)) + 8 * n * C::PITCH, kf);
+          ldsm4(ka + 1024 * n, kf);                // n > 0: d = 64 only, whose keys lie 128 bytes apart
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const uint32_t a0 = qf[mt][k][0], a1 = C::HALF ? 0u : qf[mt][k][1], a2 = qf[mt][k][RW],
@@ -405,10 +441,27 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int w = 0; w < RW; ++w) {
+          const int i = __shfl_sync(0xffffffffu, my_i, mt * 16 + w * 8 + (lane >> 2));
+          const int lim = a.causal ? at.len - a.N + i : at.len - 1;   // last key the row sees
 #pragma unroll
-          for (int e = 0; e < 2 * RW; ++e)
-            if (key0 + 8 * n + (e & 1) > lim[mt][e >> 1]) s[mt][n][e] = -INFINITY;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (key0 + 8 * n + e > lim) s[mt][n][2 * w + e] = -INFINITY;
+        }
+      // values behind the end: P is 0 there, but 0 * NaN is not
+      const int left = at.len - at.tile * KT;
+      if (left < KT) {
+#pragma unroll 1
+        for (int e = lane; e < (KT - left) * (D / 8); e += 32) {
+          const int key = left + e / (D / 8), ch = e % (D / 8);
+          *reinterpret_cast<uint4*>(smem + warp * C::RING + (ks - ring) + C::TILE + key_at(key) + ch / 8 * piece + ch % 8 * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();                  // before TMA writes the stage again
+        __syncwarp();
+      }
     }
     // ---- online softmax
     bool grew = false;
@@ -466,12 +519,10 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
             p[mt][2 * x + 1] = pack_bf16x2(y[2], y[3]);
           }
         }
-      const int row = lane & 15;
-      const uint32_t va = vs + (16 * kk + row) * C::PITCH + (((lane >> 4) ^ (row & 7)) << 4);
 #pragma unroll
       for (int n = 0; n < D / 8; n += 2) {
         uint32_t vf[4];
-        ldsm4_t(va ^ (16 * n), vf);
+        ldsm4_t(((ks + v_lane + n / 8 * piece) ^ (16 * (n % 8))) + 2048 * kk, vf);   // kk > 0: d = 64 only
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           mma_bf16(acc[mt][n], p[mt][0], p[mt][1], p[mt][2], p[mt][3], vf[0], vf[1]);
@@ -495,7 +546,8 @@ fa_paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 // reads the weight of one partial, all lanes its columns.
 template <int D>
 __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedArgs a, int rm, int per_row) {
-  constexpr int V = D / 32;                        // columns of a lane: V lane .. V lane + V - 1
+  constexpr int V = D / 32, W = V < 4 ? V : 4;     // columns of a lane: in pieces of W (8 or 16 bytes)
+  auto col = [](int lane, int e) { return e / W * 32 * W + W * lane + e % W; };
   __shared__ float so[8][D];
   __shared__ float2 sml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -515,7 +567,8 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
     b = static_cast<int>(bh / a.H);
     const int h = hq / a.group, rr = (hq - h * a.group) * a.N + i, rt = rr / rm;
     const int2 mt = a.meta[(static_cast<long long>(rt) * a.B + b) * a.H_kv + h];
-    more = mt.y;
+    // (a warp that gave up waiting left no entry: what stands there may be anything)
+    more = mt.x >= 0 && mt.y > 0 && mt.y < a.workers && mt.x < a.workers - mt.y ? mt.y : 0;
     // partial j of the row: the first lies in slot 1 of its worker, the others in slot 0 of the workers behind it
     const long long first = (static_cast<long long>(rt) * a.workers + mt.x) * 2 * a.part_rows + rr - rt * rm;
     for (int j0 = 0; more > 0 && j0 <= more; j0 += 32 * per_row) {
@@ -539,19 +592,20 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
       for (int j = 0; j < cnt; ++j) {
         const int p = j0 + sub + j * per_row;
         const float f = __shfl_sync(0xffffffffu, w, j);
-        const float* src = a.part_o + (first + (2LL * p + (p == 0 ? 1 : 0)) * a.part_rows) * D + V * lane;
+        const float* src = a.part_o + (first + (2LL * p + (p == 0 ? 1 : 0)) * a.part_rows) * D;
+        struct __align__(4 * W) Piece { float x[W]; };
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(src + e);
-          acc[e] = fmaf(f, x.x, acc[e]);
-          acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
+        for (int e = 0; e < V; e += W) {
+          const Piece x = *reinterpret_cast<const Piece*>(src + col(lane, e));
+#pragma unroll
+          for (int u = 0; u < W; ++u) acc[e + u] = fmaf(f, x.x[u], acc[e + u]);
         }
       }
     }
   }
   if (per_row > 1) {                               // the row's warps in order: results do not depend on timing
 #pragma unroll
-    for (int e = 0; e < V; ++e) so[warp][V * lane + e] = acc[e];
+    for (int e = 0; e < V; ++e) so[warp][col(lane, e)] = acc[e];
     if (lane == 0) sml[warp] = make_float2(m, l);
     __syncthreads();
     if (sub != 0) return;
@@ -566,14 +620,15 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
       const float f = exp2f(sml[warp + w].x - nb);
       l = fmaf(f, sml[warp + w].y, l);
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, so[warp + w][V * lane + e], acc[e]);
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, so[warp + w][col(lane, e)], acc[e]);
     }
   }
   if (more == 0) return;                           // written by the warp that had the whole pair
   const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-  __nv_bfloat16* o = a.o + row_offset(a.so, b, hq, i) + V * lane;
+  __nv_bfloat16* o = a.o + row_offset(a.so, b, hq, i);
 #pragma unroll
-  for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < V; e += 2)
+    *reinterpret_cast<uint32_t*>(o + col(lane, e)) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 

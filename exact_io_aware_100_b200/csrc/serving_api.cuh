@@ -93,9 +93,9 @@ PagedPlan paged_plan(const fa_paged_layout& L) {
   p.rm = paged_row_tile(L.d, rows);
   p.row_tiles = (rows + p.rm - 1) / p.rm;
   p.part_rows = rows < p.rm ? rows : p.rm;
-  // A range's partial (4 d bytes a row, written and read) should cost a quarter of its keys (4 d bytes each) at most
+  // A range's partial (4 d bytes a row) should be no more than half of its keys (4 d bytes each)
   const int kt = L.d == 64 ? 32 : 16;
-  p.min_units = std::max(kPagedMinUnits, 8 * p.part_rows / kt);
+  p.min_units = std::max(kPagedMinUnits, 2 * p.part_rows / kt);
   // no more warps than the longest sequences that the table can hold give work to
   const long long units = ((1LL * L.max_pages * L.page_size + kt - 1) / kt + kPagedPairUnits) * L.B * L.H_kv;
   const long long ctas = (units + 4 * p.min_units - 1) / (4 * p.min_units);
@@ -108,8 +108,26 @@ PagedPlan paged_plan(const fa_paged_layout& L) {
   return p;
 }
 
+// 5-D map of a cache's K or V pages, {64 columns, row, 64-column piece, head, page}, so that one box brings `box` keys of
+// all d columns as pieces of 128-byte rows.
+bool make_map_pages(CUtensorMap* m, const void* base, const fa_paged_layout& L, const fa_strides& st, int box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dense = static_cast<cuuint64_t>(L.d) * 2;
+  cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(L.page_size), static_cast<cuuint64_t>(L.d / 64),
+                        static_cast<cuuint64_t>(L.H_kv), static_cast<cuuint64_t>(L.num_pages)};
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(st.row) * 2, 128, L.H_kv > 1 ? static_cast<cuuint64_t>(st.head) * 2 : dense,
+                           L.num_pages > 1 ? static_cast<cuuint64_t>(st.batch) * 2 : dense};
+  cuuint32_t extent[5] = {64, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(L.d / 64), 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, extent, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 template <int D, int RM>
-fa_status launch_paged(const PagedArgs& a, bool* attr, cudaStream_t s) {
+fa_status launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, bool* attr, cudaStream_t s) {
   using C = PagedCfg<D, RM>;
   if (!*attr) {
     if (cudaFuncSetAttribute(fa_paged_decode_kernel<D, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
@@ -117,7 +135,7 @@ fa_status launch_paged(const PagedArgs& a, bool* attr, cudaStream_t s) {
       return FA_ERR_CUDA;
     *attr = true;
   }
-  fa_paged_decode_kernel<D, RM><<<dim3(a.workers / C::WARPS, a.row_tiles), C::THREADS, C::SMEM, s>>>(a);
+  fa_paged_decode_kernel<D, RM><<<dim3(a.workers / C::WARPS, a.row_tiles), C::THREADS, C::SMEM, s>>>(tk, tv, a);
   // the merge: 8, 4, 2 or 1 warps to a row, as many as the GPU holds at once; launched while the first kernel runs
   const long long rows = 1LL * a.B * a.H * a.N;
   const int per_row = rows <= kPagedSms * 8 ? 8 : rows <= kPagedSms * 16 ? 4 : rows <= kPagedSms * 32 ? 2 : 1;
@@ -336,17 +354,23 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   a.part_ml = reinterpret_cast<float2*>(w + plan.o_bytes);
   a.meta = reinterpret_cast<int2*>(w + plan.o_bytes + plan.ml_bytes);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int kt = L.d == 64 ? 32 : 16;
+  a.box = L.page_size % kt == 0 ? kt : L.page_size % 16 == 0 ? 16 : 8;
+  a.wait_limit_ns = kWaitLimitNs;
+  CUtensorMap tk, tv;
+  if (!make_map_pages(&tk, k_pages, L, L.k_pages, a.box) || !make_map_pages(&tv, v_pages, L, L.v_pages, a.box))
+    return FA_ERR_CUDA;
   const int di = L.d == 64 ? 0 : L.d == 128 ? 1 : 2, ri = plan.rm == 8 ? 0 : plan.rm == 16 ? 1 : 2;
   bool* attr = &ds->paged_attr[di][ri];
   switch (di * 3 + ri) {
-    case 0: return launch_paged<64, 8>(a, attr, s);
-    case 1: return launch_paged<64, 16>(a, attr, s);
-    case 2: return launch_paged<64, 32>(a, attr, s);
-    case 3: return launch_paged<128, 8>(a, attr, s);
-    case 4: return launch_paged<128, 16>(a, attr, s);
-    case 5: return launch_paged<128, 32>(a, attr, s);
-    case 6: return launch_paged<256, 8>(a, attr, s);
-    default: return launch_paged<256, 16>(a, attr, s);
+    case 0: return launch_paged<64, 8>(tk, tv, a, attr, s);
+    case 1: return launch_paged<64, 16>(tk, tv, a, attr, s);
+    case 2: return launch_paged<64, 32>(tk, tv, a, attr, s);
+    case 3: return launch_paged<128, 8>(tk, tv, a, attr, s);
+    case 4: return launch_paged<128, 16>(tk, tv, a, attr, s);
+    case 5: return launch_paged<128, 32>(tk, tv, a, attr, s);
+    case 6: return launch_paged<256, 8>(tk, tv, a, attr, s);
+    default: return launch_paged<256, 16>(tk, tv, a, attr, s);
   }
 }
 
