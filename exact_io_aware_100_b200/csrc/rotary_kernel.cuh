@@ -46,7 +46,7 @@ __device__ __forceinline__ float2 rot_cos_sin(double f, int pos, float magnitude
   const float half_turns = static_cast<float>(static_cast<int>(where >> 32)) * 4.656612873077393e-10f;   // 2^-31
   float s, c;
   sincospif(half_turns, &s, &c);
-  return make_float2(c * magnitude, (inverse ? -s : s) * magnitude);
+  return make_float2(__fmul_rn(c, magnitude), __fmul_rn(inverse ? -s : s, magnitude));
 }
 
 template <typename T>
@@ -135,9 +135,9 @@ __device__ __forceinline__ RotHead rot_head(const RotArgs& a, const RotToken& tk
           static_cast<T*>(a.vo) + row_offset(a.svo, ob, h - a.H_kv, orow), false};
 }
 
-// The pair of elements (xa, xb) turned.
+// The pair of elements (xa, xb) turned, with the roundings fixed, so that every path gives the same bits.
 __device__ __forceinline__ float2 rot_turn(float xa, float xb, float2 cs) {
-  return make_float2(xa * cs.x - xb * cs.y, xb * cs.x + xa * cs.y);
+  return make_float2(__fmaf_rn(xa, cs.x, -__fmul_rn(xb, cs.y)), __fmaf_rn(xb, cs.x, __fmul_rn(xa, cs.y)));
 }
 
 // Any alignment and any even r: one thread per (token, pair of columns, chunk of heads); thread p of a token takes pair
