@@ -1,9 +1,10 @@
 """Serving operators of libfa.so: rotary positions, a paged key/value cache, the attention that reads it and
 the bookkeeping of its pages.
 
-As in the rest of the binding, Python only checks and marshals arguments.  Low-level names mirror ``include/fa.h``
-(``fa_rotary``, ``fa_paged_append``, ``fa_paged_decode``, ``fa_pages_*``); ``rotary``, ``paged_append``, ``paged_decode``
-and ``pages_*`` build the layouts and allocate the outputs.
+As in the rest of the binding, nothing is computed here.  Low-level names mirror ``include/fa.h`` (``fa_rotary``,
+``fa_paged_append``, ``fa_paged_decode``, ``fa_pages_*``); ``rotary``, ``paged_append``, ``paged_decode`` and ``pages_*``
+check the tensors, build the layouts and allocate the outputs, in ``_serving.so`` (csrc/serving_binding.cpp), because a
+generation step makes several of these calls and their kernels take a few microseconds each.
 
 A serving step of a batch of sequences, all of it on the device and capturable into a CUDA graph:
 
@@ -137,29 +138,39 @@ def fa_pages_copy(k_pages, v_pages, copies, layout: FaPagedLayout, stream=None) 
 
 
 # ----------------------------------------------------------------- where a call runs
-class _Here:
-    """The tensors' device is the current one and its current stream is meant: nothing to set up."""
-    __slots__ = ()
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
+_ext = None
 
 
-class _There:
-    """Makes the tensors' device and ``stream`` (if given) current for a call.  Tensors used on a stream of the caller's
-    are recorded as in use there."""
+def _native():
+    """The extension module, its functions bound to libfa.so's."""
+    global _ext
+    if _ext is None:
+        import torch  # noqa: F401 (its libraries)
+        try:
+            from . import _serving
+        except ImportError as e:
+            raise RuntimeError("_serving.so is not built; run `python -m exact_io_aware_100_b200.build`") from e
+        L = _fa.load_library()
+        _serving.bind(_fa.FaError, *(ctypes.cast(getattr(L, name), _VP).value for name in (
+            "fa_rotary", "fa_paged_append", "fa_paged_decode", "fa_paged_decode_workspace_size", "fa_pages_workspace_size",
+            "fa_pages_extend", "fa_pages_fork", "fa_pages_free", "fa_pages_compact", "fa_pages_copy")))
+        _ext = _serving
+    return _ext
+
+
+class _On:
+    """Makes the caller's ``stream`` (of torch, or a handle) current for a call on `tensors`, which are recorded as in use
+    there."""
     __slots__ = ("guards", "tensors", "stream")
 
-    def __init__(self, stream, device, tensors):
+    def __init__(self, stream, *tensors):
         import torch
-        self.guards = (torch.cuda.device(device),)
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.guards += (torch.cuda.stream(stream),)
+        device = tensors[0].get_device()
+        if device < 0:
+            raise ValueError("expected a CUDA tensor: the library reads and writes device memory only")
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self.guards = (torch.cuda.device(device), torch.cuda.stream(stream))
         self.tensors, self.stream = tensors, stream
 
     def __enter__(self):
@@ -167,65 +178,13 @@ class _There:
             g.__enter__()
 
     def __exit__(self, *exc):
-        if self.stream is not None and exc[0] is None:
-            import torch
-            if not torch.cuda.is_current_stream_capturing():   # a graph keeps its own memory alive
-                for t in self.tensors:
-                    if t is not None:
-                        t.record_stream(self.stream)
+        import torch
+        if exc[0] is None and not torch.cuda.is_current_stream_capturing():   # a graph keeps its own memory alive
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
         for g in reversed(self.guards):
             g.__exit__(*exc)
-
-
-_HERE = _Here()
-
-
-def _launch(stream, *tensors):
-    """Where a call on these tensors runs, as a context; checks that they share one CUDA device."""
-    import torch
-    device = None
-    for t in tensors:
-        if t is not None:
-            index = t.get_device()
-            if index != device:
-                if index < 0:
-                    raise ValueError("expected a CUDA tensor: the library reads and writes device memory only")
-                if device is not None:
-                    raise ValueError(f"tensors on different devices: cuda:{device} and cuda:{index}")
-                device = index
-    if stream is None and device == torch.cuda.current_device():
-        return _HERE
-    return _There(stream, device, tensors)
-
-
-def _int32(t, name: str, dims: int):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != dims or (t.stride(-1) != 1 and t.numel() > 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name}: expected a {dims}-D int32 tensor, contiguous in its last axis")
-
-
-def _rows(t, name: str, dims, dtypes):
-    """Checks [B, heads, rows, d] (4-D) or packed [rows, heads, d] (3-D); d contiguous."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() not in dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name}: expected [B, heads, rows, d]" + (" or packed [rows, heads, d]" if 3 in dims else "") +
-                         " with contiguous d")
-
-
-def _st(t):
-    """(batch, head, row) strides of a 4-D or packed 3-D operand; zeros for None."""
-    if t is None:
-        return 0, 0, 0
-    s = t.stride()
-    return (s[0], s[1], s[2]) if len(s) == 4 else (0, s[1], s[0])
-
-
-def _freqs(freqs):
-    import torch
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise ValueError("freqs: expected a contiguous 1-D float64 tensor (rotary_frequencies gives one)")
-    return 2 * freqs.numel()
 
 
 # ----------------------------------------------------------------- rotary positions
@@ -275,76 +234,26 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
     return f.to(device), magnitude
 
 
-def _rotary(q, k, freqs, positions, interleaved, magnitude, out, inverse, stream):
-    import torch
-    dtypes = (torch.bfloat16, torch.float32)
-    _rows(q, "q", (3, 4), dtypes)
-    r = _freqs(freqs)
-    packed = q.dim() == 3
-    if packed:
-        N, H, d = q.shape
-        B = 1
-    else:
-        B, H, N, d = q.shape
-    H_kv = 0
-    if k is not None:
-        _rows(k, "k", (q.dim(),), (q.dtype,))
-        H_kv = k.shape[1]
-        if k.shape[0] != q.shape[0] or k.shape[-1] != d or (not packed and k.shape[2] != N):
-            raise ValueError("q and k: batch, rows and d must agree")
-    pos_batch = 0
-    if positions is not None:
-        _int32(positions, "positions", 2 if not packed and positions.dim() == 2 else 1)
-        if positions.shape[-1] != N or (positions.dim() == 2 and positions.shape[0] != B):
-            raise ValueError("positions: expected one per row ([rows] or [B, rows])")
-        pos_batch = positions.stride(0) if positions.dim() == 2 else 0
-    with _launch(stream, q, k, freqs, positions, *(out or ())):
-        if out is None:
-            q_out, k_out = torch.empty_like(q), None if k is None else torch.empty_like(k)
-        else:
-            q_out, k_out = out
-            for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-                if (x is None) != (y is None) or (x is not None and (y.shape != x.shape or y.dtype != x.dtype or
-                                                                    (d > 1 and y.stride(-1) != 1))):
-                    raise ValueError(f"out: {name} must have its input's shape and dtype, d contiguous")
-        layout = FaRotaryLayout(B, H, H_kv, N, d, r, int(bool(interleaved)), pos_batch, *_st(q), *_st(k), *_st(q_out),
-                                *_st(k_out))
-        fa_rotary(q, k, q_out, k_out, positions, freqs, layout, float(magnitude), inverse,
-                  _fa.FA_BF16 if q.dtype == torch.bfloat16 else _fa.FA_F32)
-    return q_out, k_out
-
-
 def rotary(q, k, freqs, positions=None, interleaved: bool = False, magnitude: float = 1.0, out=None, stream=None):
     """(q', k'): q [B, H, N, d] and k [B, H_kv, N, d] (bf16 or float32, any strides; or packed [rows, heads, d]; k may be
     None) with the first 2 * len(freqs) columns of every head turned by the angle position * freqs (fa_rotary).
     positions: int32 [N], [B, N], packed [rows]; None: 0 .. N - 1.  ``out``: a pair to write to, which may be (q, k)."""
-    return _rotary(q, k, freqs, positions, interleaved, magnitude, out, False, stream)
+    if stream is not None:
+        with _On(stream, q, k, freqs, positions, *(out or ())):
+            return rotary(q, k, freqs, positions, interleaved, magnitude, out)
+    return (_ext or _native()).rotary(q, k, freqs, positions, interleaved, magnitude, out, False)
 
 
 def rotary_backward(dq, dk, freqs, positions=None, interleaved: bool = False, magnitude: float = 1.0, out=None,
                     stream=None):
     """Gradients of q and k from those of ``rotary``'s outputs: the map's transpose, a turn by the negative angle."""
-    return _rotary(dq, dk, freqs, positions, interleaved, magnitude, out, True, stream)
+    if stream is not None:
+        with _On(stream, dq, dk, freqs, positions, *(out or ())):
+            return rotary_backward(dq, dk, freqs, positions, interleaved, magnitude, out)
+    return (_ext or _native()).rotary(dq, dk, freqs, positions, interleaved, magnitude, out, True)
 
 
 # ----------------------------------------------------------------- the paged cache
-def _cache(k_pages, v_pages):
-    import torch
-    _rows(k_pages, "k_pages", (4,), (torch.bfloat16,))
-    _rows(v_pages, "v_pages", (4,), (torch.bfloat16,))
-    if k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages: one shape [pages, H_kv, page_size, d]")
-    return k_pages.shape
-
-
-def _table(page_table, seq_lens, B=None):
-    _int32(page_table, "page_table", 2)
-    _int32(seq_lens, "seq_lens", 1)
-    if page_table.shape[0] != seq_lens.shape[0] or (B is not None and B != seq_lens.shape[0]):
-        raise ValueError("page_table, seq_lens and the batch must agree")
-    return page_table.shape[1]
-
-
 def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q=None, freqs=None, interleaved: bool = False,
                  magnitude: float = 1.0, cu_seqlens=None, out=None, stream=None):
     """Writes new keys and values (bf16) into the cache k_pages, v_pages [pages, H_kv, page_size, d] (any strides; pages of
@@ -355,125 +264,65 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q=None, freqs=Non
     keys, and q [B, H, N, d] (or packed), are turned as by ``rotary`` at those positions.  A token whose position would
     be negative is padding: not written, and zero in the returned q; so are packed rows outside every sequence, which keep
     their values when ``out`` is q itself."""
-    import torch
-    P, H_kv, page, d = _cache(k_pages, v_pages)
-    packed = cu_seqlens is not None
-    for name, t in (("k", k), ("v", v)):
-        _rows(t, name, (3 if packed else 4,), (torch.bfloat16,))
-        if t.shape[1] != H_kv or t.shape[-1] != d or t.shape != k.shape:
-            raise ValueError("k and v: heads and d as in the cache, one shape")
-    B = cu_seqlens.numel() - 1 if packed else k.shape[0]
-    M = _table(page_table, seq_lens, B)
-    if packed:
-        _int32(cu_seqlens, "cu_seqlens", 1)
-    if q is not None:
-        _rows(q, "q", (k.dim(),), (torch.bfloat16,))
-        if q.shape[0] != k.shape[0] or q.shape[-1] != d or (not packed and q.shape[2] != k.shape[2]):
-            raise ValueError("q and k: batch, rows and d must agree")
-    r = 0 if freqs is None else _freqs(freqs)
-    with _launch(stream, q, k, v, k_pages, v_pages, page_table, seq_lens, freqs, cu_seqlens, out):
-        if out is None:
-            out = None if q is None else torch.empty_like(q)
-        elif q is None or out.shape != q.shape or out.dtype != q.dtype or (d > 1 and out.stride(-1) != 1):
-            raise ValueError("out: must have q's shape and dtype, d contiguous")
-        layout = FaPagedLayout(B, 0 if q is None else q.shape[1], H_kv, d, 0 if packed else k.shape[2], P, page, M,
-                               page_table.stride(0), *_st(q), *_st(out), *_st(k), *_st(v), *k_pages.stride()[:3],
-                               *v_pages.stride()[:3], _fa._ptr(cu_seqlens), k.shape[0] if packed else 0, r,
-                               int(bool(interleaved)))
-        fa_paged_append(q, k, v, out, k_pages, v_pages, page_table, seq_lens, freqs, layout, float(magnitude))
-    return out
+    if stream is not None:
+        with _On(stream, k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, cu_seqlens, out):
+            return paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, interleaved, magnitude, cu_seqlens,
+                                out)
+    return (_ext or _native()).paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, interleaved, magnitude,
+                                            cu_seqlens, out)
 
 
 def paged_decode(q, k_pages, v_pages, page_table, seq_lens, causal: bool = True, scale: float | None = None, stream=None,
                  workspace=None):
     """O, lse of the last N positions q [B, H, N, d] of each sequence against its seq_lens[b] cached keys (bf16; H a
     multiple of the cache's H_kv).  Rows that see no key (an empty sequence) give O = 0, lse = -inf."""
-    import torch
-    P, H_kv, page, d = _cache(k_pages, v_pages)
-    _rows(q, "q", (4,), (torch.bfloat16,))
-    B, H, N, dq = q.shape
-    if dq != d:
-        raise ValueError("q and the cache: d must agree")
-    M = _table(page_table, seq_lens, B)
-    with _launch(stream, q, k_pages, v_pages, page_table, seq_lens, workspace):
-        o = torch.empty_like(q)
-        lse = q.new_empty((B, H, N), dtype=torch.float32)
-        layout = FaPagedLayout(B, H, H_kv, d, N, P, page, M, page_table.stride(0), *_st(q), *_st(o), 0, 0, 0, 0, 0, 0,
-                               *k_pages.stride()[:3], *v_pages.stride()[:3], None, 0, 0, 0)
-        if workspace is None:
-            workspace = _fa._workspace(fa_paged_decode_workspace_size(layout), q.device)
-        fa_paged_decode(q, k_pages, v_pages, page_table, seq_lens, o, lse, layout, causal, workspace, scale)
-    return o, lse
+    if stream is not None:
+        with _On(stream, q, k_pages, v_pages, page_table, seq_lens, workspace):
+            return paged_decode(q, k_pages, v_pages, page_table, seq_lens, causal, scale, None, workspace)
+    return (_ext or _native()).paged_decode(q, k_pages, v_pages, page_table, seq_lens, causal, scale, workspace)
 
 
 # ----------------------------------------------------------------- bookkeeping of pages
-def _pages_state(page_table, seq_lens, refcounts, page_size, *requests):
-    M = _table(page_table, seq_lens)
-    _int32(refcounts, "refcounts", 1)
-    for name, t in requests:
-        _int32(t, name, 1)
-        if t.numel() != requests[0][1].numel():
-            raise ValueError(f"{requests[0][0]} and {name}: one length")
-    return FaPagesLayout(page_table.shape[0], refcounts.numel(), int(page_size), M, page_table.stride(0))
-
-
-def _pages_workspace(layout, n, workspace, device):
-    return _fa._workspace(fa_pages_workspace_size(layout, n), device) if workspace is None else workspace
-
-
 def pages_extend(page_table, seq_lens, refcounts, page_size: int, seqs, tokens, stream=None, workspace=None):
     """Sequences ``seqs`` (int32 [n]) grow by ``tokens`` (int32 [n]) positions and get the pages they need: the free ones
     of lowest number, in the order of the requests.  page_table [S, max_pages], seq_lens [S] and refcounts [pages] (int32)
     are updated in place.  Returns status int32 [n]: FA_OK, FA_ERR_WORKSPACE (no page left) or FA_ERR_INVALID; a request
     that is not FA_OK changed nothing."""
-    import torch
-    layout = _pages_state(page_table, seq_lens, refcounts, page_size, ("seqs", seqs), ("tokens", tokens))
-    with _launch(stream, page_table, seq_lens, refcounts, seqs, tokens, workspace):
-        status = torch.empty_like(seqs)
-        fa_pages_extend(page_table, seq_lens, refcounts, layout, seqs, tokens, status,
-                        _pages_workspace(layout, seqs.numel(), workspace, seqs.device))
-    return status
+    if stream is not None:
+        with _On(stream, page_table, seq_lens, refcounts, seqs, tokens, workspace):
+            return pages_extend(page_table, seq_lens, refcounts, page_size, seqs, tokens, None, workspace)
+    return (_ext or _native()).pages_extend(page_table, seq_lens, refcounts, page_size, seqs, tokens, workspace)
 
 
 def pages_fork(page_table, seq_lens, refcounts, page_size: int, src, dst, stream=None, workspace=None):
     """The empty sequences ``dst`` (int32 [n]) become copies of ``src``: whole pages are shared, a last page that is not
     full gets a page of its own.  Returns (copies int32 [n, 3], status int32 [n]); ``pages_copy`` with ``copies`` then
     brings the contents over, in each layer's cache."""
-    import torch
-    layout = _pages_state(page_table, seq_lens, refcounts, page_size, ("src", src), ("dst", dst))
-    with _launch(stream, page_table, seq_lens, refcounts, src, dst, workspace):
-        status = torch.empty_like(src)
-        copies = torch.empty((src.numel(), 3), dtype=torch.int32, device=src.device)
-        fa_pages_fork(page_table, seq_lens, refcounts, layout, src, dst, copies, status,
-                      _pages_workspace(layout, src.numel(), workspace, src.device))
-    return copies, status
+    if stream is not None:
+        with _On(stream, page_table, seq_lens, refcounts, src, dst, workspace):
+            return pages_fork(page_table, seq_lens, refcounts, page_size, src, dst, None, workspace)
+    return (_ext or _native()).pages_fork(page_table, seq_lens, refcounts, page_size, src, dst, workspace)
 
 
 def pages_free(page_table, seq_lens, refcounts, page_size: int, seqs, stream=None) -> None:
     """Sequences ``seqs`` (int32 [n]) become empty; their pages are free once no other sequence holds them."""
-    layout = _pages_state(page_table, seq_lens, refcounts, page_size, ("seqs", seqs))
-    with _launch(stream, page_table, seq_lens, refcounts, seqs):
-        fa_pages_free(page_table, seq_lens, refcounts, layout, seqs)
+    if stream is not None:
+        with _On(stream, page_table, seq_lens, refcounts, seqs):
+            return pages_free(page_table, seq_lens, refcounts, page_size, seqs)
+    (_ext or _native()).pages_free(page_table, seq_lens, refcounts, page_size, seqs)
 
 
 def pages_compact(page_table, seq_lens, refcounts, page_size: int, stream=None, workspace=None):
     """Moves the pages in use to the lowest numbers.  Returns copies int32 [pages // 2, 3] for ``pages_copy``."""
-    import torch
-    layout = _pages_state(page_table, seq_lens, refcounts, page_size)
-    with _launch(stream, page_table, seq_lens, refcounts, workspace):
-        copies = torch.empty((refcounts.numel() // 2, 3), dtype=torch.int32, device=refcounts.device)
-        fa_pages_compact(page_table, seq_lens, refcounts, layout, copies,
-                         _pages_workspace(layout, 0, workspace, refcounts.device))
-    return copies
+    if stream is not None:
+        with _On(stream, page_table, seq_lens, refcounts, workspace):
+            return pages_compact(page_table, seq_lens, refcounts, page_size, None, workspace)
+    return (_ext or _native()).pages_compact(page_table, seq_lens, refcounts, page_size, workspace)
 
 
 def pages_copy(k_pages, v_pages, copies, stream=None) -> None:
     """Copies pages within k_pages, v_pages [pages, H_kv, page_size, d] (any strides) as ``copies`` lists them."""
-    P, H_kv, page, d = _cache(k_pages, v_pages)
-    _int32(copies, "copies", 2)
-    if copies.shape[1] != 3 or not copies.is_contiguous():
-        raise ValueError("copies: expected a contiguous [n, 3] tensor")
-    with _launch(stream, k_pages, v_pages, copies):
-        layout = FaPagedLayout(1, 0, H_kv, d, 0, P, page, 0, 0, *(0,) * 12, *k_pages.stride()[:3],
-                               *v_pages.stride()[:3], None, 0, 0, 0)
-        fa_pages_copy(k_pages, v_pages, copies, layout)
+    if stream is not None:
+        with _On(stream, k_pages, v_pages, copies):
+            return pages_copy(k_pages, v_pages, copies)
+    (_ext or _native()).pages_copy(k_pages, v_pages, copies)

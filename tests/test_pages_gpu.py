@@ -253,3 +253,52 @@ def test_a_serving_loop(graph):
     for _ in range(2):
         run([2, 3, 5])
     _ok()
+
+
+def test_low_level_names_give_the_same():
+    """The mirrors of the C ABI, with layouts and workspaces of the caller's, against the calls that make their own."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    S, P, M, page, H, H_kv, d = 3, 12, 4, 16, 4, 2, 64
+    freqs, _ = fa.rotary_frequencies(d)
+    q, k, v = (torch.randn(S, h, 5, d, device="cuda").bfloat16() for h in (H, H_kv, H_kv))
+    strides = lambda *ts: [s for t in ts for s in (t.stride()[:3] if t is not None else (0, 0, 0))]  # noqa: E731
+    yq, yk = torch.empty_like(q), torch.empty_like(k)
+    fa.fa_rotary(q, k, yq, yk, None, freqs, fa.FaRotaryLayout(S, H, H_kv, 5, d, d, 0, 0, *strides(q, k, yq, yk)), 1.0, False,
+                 fa.FA_BF16)
+    want = fa.rotary(q, k, freqs)
+    assert torch.equal(yq, want[0]) and torch.equal(yk, want[1])
+
+    def run(low):
+        table = torch.full((S, M), -1, dtype=torch.int32, device="cuda")
+        lens, refs = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (S, P))
+        kp, vp = (torch.zeros(P, H_kv, page, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        seqs, tokens, src, dst = _i([0, 1]), _i([21, 7]), _i([0]), _i([2])
+        if not low:
+            status = fa.pages_extend(table, lens, refs, page, seqs, tokens)
+            copies, forked = fa.pages_fork(table, lens, refs, page, src, dst)
+            fa.pages_copy(kp, vp, copies)
+            turned = fa.paged_append(k, v, kp, vp, table, lens, q=q, freqs=freqs)
+            o, lse = fa.paged_decode(turned, kp, vp, table, lens)
+            fa.pages_free(table, lens, refs, page, seqs)
+            moves = fa.pages_compact(table, lens, refs, page)
+        else:
+            G = fa.FaPagesLayout(S, P, page, M, M)
+            ws = torch.empty(fa.fa_pages_workspace_size(G, 2), dtype=torch.uint8, device="cuda")
+            status, forked, copies = torch.empty_like(seqs), torch.empty_like(src), torch.empty(1, 3, dtype=torch.int32, device="cuda")
+            fa.fa_pages_extend(table, lens, refs, G, seqs, tokens, status, ws)
+            fa.fa_pages_fork(table, lens, refs, G, src, dst, copies, forked, ws)
+            turned, o = torch.empty_like(q), torch.empty_like(q)
+            lse = torch.empty(S, H, 5, device="cuda")
+            L = fa.FaPagedLayout(S, H, H_kv, d, 5, P, page, M, M, *strides(q, o, k, v, kp, vp), None, 0, d, 0)
+            fa.fa_pages_copy(kp, vp, copies, L)
+            fa.fa_paged_append(q, k, v, turned, kp, vp, table, lens, freqs, L)
+            big = torch.empty(fa.fa_paged_decode_workspace_size(L), dtype=torch.uint8, device="cuda")
+            fa.fa_paged_decode(turned, kp, vp, table, lens, o, lse, L, True, big)
+            fa.fa_pages_free(table, lens, refs, G, seqs)
+            moves = torch.empty(P // 2, 3, dtype=torch.int32, device="cuda")
+            fa.fa_pages_compact(table, lens, refs, G, moves, ws)
+        return table, lens, refs, kp, vp, status, copies, forked, turned, o, lse, moves
+
+    assert all(torch.equal(x, y) for x, y in zip(run(False), run(True)))
+    _ok()
