@@ -36,6 +36,7 @@ struct DevState {
   bool bwd256_attr[2] = {};                        // [packed]
   bool fwd256_attr[2] = {};                        // [packed]
   bool dec_attr = false, decw_attr = false;
+  bool rotary_attr[12] = {};                       // [vector kind + 3 append + 6 interleaved]
   bool paged_attr[3][3] = {};                      // [d 64, 128, 256][row tile 8, 16, 32]
 };
 DevState g_dev[kMaxDevices];

@@ -28,11 +28,22 @@ bool vec_rows(const void* p, const Strides& st, int batch, int heads, int rows, 
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ok(st.b, batch) && ok(st.h, heads) && ok(st.r, rows);
 }
 
-// heads_per: heads of a thread.  A thread forms its angles once for all of its heads, so many heads save arithmetic, and
-// few give the GPU more threads to hide latency with: as many heads as leave kRotaryThreads threads, 4 to 16.
-constexpr long long kRotaryThreads = 148LL * 2048 * 2;
+template <typename T, int V, bool APPEND, bool INTER>
+fa_status launch_rotary_vec(const RotArgs& a, dim3 grid, int heads_per, DevState* ds, cudaStream_t stream) {
+  constexpr int kMost = kRotHeads * 2 * kRotThreads * V * sizeof(T), id = (sizeof(T) == 4 ? 0 : V == 4 ? 1 : 2) + 3 * APPEND + 6 * INTER;
+  if (!ds->rotary_attr[id]) {
+    if (cudaFuncSetAttribute(fa_rotary_vec_kernel<T, V, APPEND, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) !=
+        cudaSuccess)
+      return FA_ERR_CUDA;
+    ds->rotary_attr[id] = true;
+  }
+  fa_rotary_vec_kernel<T, V, APPEND, INTER>
+      <<<grid, kRotThreads, kMost / kRotHeads * heads_per, stream>>>(a, heads_per);
+  return launched();
+}
+
 template <typename T, bool APPEND>
-fa_status launch_rotary(const RotArgs& a, int interleaved, cudaStream_t stream) {
+fa_status launch_rotary(const RotArgs& a, int interleaved, DevState* ds, cudaStream_t stream) {
   constexpr int es = sizeof(T), V = 16 / es;
   const int heads = a.H + (APPEND ? 2 : 1) * a.H_kv;
   const int rows = APPEND && a.cu != nullptr ? a.total : a.N, nb = APPEND && a.cu != nullptr ? 1 : a.B;
@@ -42,21 +53,22 @@ fa_status launch_rotary(const RotArgs& a, int interleaved, cudaStream_t stream) 
            (a.H_kv == 0 || APPEND || (rows_ok(a.k, a.sk, a.H_kv) && rows_ok(a.ko, a.sko, a.H_kv)));
   };
   const int v = fits(V) ? V : es == 2 && fits(4) ? 4 : 0;
-  const long long per = v ? a.d / (2 * v) : a.r / 2 + a.d - a.r;
-  const long long blocks = (a.tokens * per + 255) / 256;
+  const long long per = v ? a.d / (2 * v) : a.r / 2 + a.d - a.r, blocks = (a.tokens * per + kRotThreads - 1) / kRotThreads;
   if (blocks >= (1LL << 31)) return FA_ERR_INVALID;
-  const long long most = blocks * 256 * heads / kRotaryThreads, least = heads / 65535 + 1;
-  const int heads_per = static_cast<int>(std::max(std::min(std::max(most, 4LL), 16LL), least));
+  // heads of a thread: kRotHeads, evenly over the chunks; fewer while there are not two blocks to an SM
+  const long long few = std::max(1LL, blocks * heads / (2 * kPagedSms));
+  const long long chunks = (heads + std::min<long long>(few, kRotHeads) - 1) / std::min<long long>(few, kRotHeads);
+  const int heads_per = static_cast<int>((heads + chunks - 1) / chunks);
   const dim3 grid(static_cast<unsigned>(blocks), (heads + heads_per - 1) / heads_per);
-  if (v == 0)
-    fa_rotary_kernel<T, APPEND><<<grid, 256, 0, stream>>>(a, interleaved, heads_per);
-  else if (v == V)
-    (interleaved ? fa_rotary_vec_kernel<T, V, APPEND, true> : fa_rotary_vec_kernel<T, V, APPEND, false>)
-        <<<grid, 256, 0, stream>>>(a, heads_per);
-  else
-    (interleaved ? fa_rotary_vec_kernel<T, 4, APPEND, true> : fa_rotary_vec_kernel<T, 4, APPEND, false>)
-        <<<grid, 256, 0, stream>>>(a, heads_per);
-  return launched();
+  if (v == 0) {
+    fa_rotary_kernel<T, APPEND><<<grid, kRotThreads, 0, stream>>>(a, interleaved, heads_per);
+    return launched();
+  }
+  if (v == V)
+    return interleaved ? launch_rotary_vec<T, V, APPEND, true>(a, grid, heads_per, ds, stream)
+                       : launch_rotary_vec<T, V, APPEND, false>(a, grid, heads_per, ds, stream);
+  return interleaved ? launch_rotary_vec<T, 4, APPEND, true>(a, grid, heads_per, ds, stream)
+                     : launch_rotary_vec<T, 4, APPEND, false>(a, grid, heads_per, ds, stream);
 }
 
 // The cache and table of a paged layout.
@@ -208,7 +220,7 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
                     fa_dtype dtype, fa_stream_t stream) {
   if (layout == nullptr) return FA_ERR_INVALID;
   const fa_rotary_layout& L = *layout;
-  if (L.B < 1 || L.H < 1 || L.H_kv < 0 || L.H >= (1 << 24) || L.H_kv >= (1 << 24) || L.N < 0 || L.d < 1 || L.d > 1024 || L.rotary_dim < 0 || L.rotary_dim > L.d ||
+  if (L.B < 1 || L.H < 1 || L.H_kv < 0 || L.H >= (1 << 18) || L.H_kv >= (1 << 18) || L.N < 0 || L.d < 1 || L.d > 1024 || L.rotary_dim < 0 || L.rotary_dim > L.d ||
       L.rotary_dim % 2 != 0 || 1LL * L.B * L.N >= (1LL << 31) || !std::isfinite(magnitude) ||
       !out_strides_ok(L.q_out, L.B, L.H, L.N) || (L.H_kv > 0 && !out_strides_ok(L.k_out, L.B, L.H_kv, L.N)))
     return FA_ERR_INVALID;
@@ -239,9 +251,12 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
   a.tokens = 1LL * L.B * L.N;
   a.magnitude = magnitude;
   a.inverse = inverse;
+  DevState* ds = nullptr;
+  const fa_status st = device_state(&ds);
+  if (st != FA_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dtype == FA_F32 ? launch_rotary<float, false>(a, L.interleaved, s)
-                         : launch_rotary<__nv_bfloat16, false>(a, L.interleaved, s);
+  return dtype == FA_F32 ? launch_rotary<float, false>(a, L.interleaved, ds, s)
+                         : launch_rotary<__nv_bfloat16, false>(a, L.interleaved, ds, s);
 }
 
 fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, void* k_pages, void* v_pages,
@@ -253,7 +268,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
   if (st != FA_OK) return st;
   const bool pk = L.cu_seqlens != nullptr;
   const long long tokens = pk ? L.total : 1LL * L.B * L.N;
-  if ((pk ? L.total : L.N) < 0 || tokens >= (1LL << 31) || (q != nullptr && (L.H < 1 || L.H >= (1 << 24))) || L.H_kv >= (1 << 24) || !std::isfinite(magnitude) ||
+  if ((pk ? L.total : L.N) < 0 || tokens >= (1LL << 31) || (q != nullptr && (L.H < 1 || L.H >= (1 << 18))) || L.H_kv >= (1 << 18) || !std::isfinite(magnitude) ||
       (freqs != nullptr && (L.rotary_dim < 0 || L.rotary_dim > L.d || L.rotary_dim % 2 != 0)))
     return FA_ERR_INVALID;
   if (tokens == 0) return FA_OK;
@@ -297,7 +312,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
   a.page = L.page_size;
   a.max_pages = L.max_pages;
   a.status = ds->status;
-  return launch_rotary<__nv_bfloat16, true>(a, L.interleaved, static_cast<cudaStream_t>(stream));
+  return launch_rotary<__nv_bfloat16, true>(a, L.interleaved, ds, static_cast<cudaStream_t>(stream));
 }
 
 size_t fa_paged_decode_workspace_size(const fa_paged_layout* layout) {
