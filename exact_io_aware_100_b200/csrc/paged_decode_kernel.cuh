@@ -78,13 +78,17 @@ struct PagedCfg {
   static constexpr int KT = D == 64 ? 32 : 16;   // keys per tile
   static constexpr int NT = KT / 8;
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
-  static constexpr int STAGES = 3;
+  // A slot of the ring holds the K and the V tile of some keys, or (d = 256, whose tiles are 8 KB) one of them, K and V in
+  // turn: two blocks to an SM either way.  (d = 256, 32 rows: 177 us for 536 MB with one block of 48 KB rings, 128 us so;
+  // d = 128, 16 x 8192 keys: 95 us with both tiles in a slot, 98 us with slots of one.)
+  static constexpr bool SPLIT = D == 256;
+  static constexpr int SLOTS = 3;
   static constexpr int PITCH = 2 * D;            // bytes of a key, or of a query
   static constexpr int TILE = KT * PITCH;        // [box][64 columns][key][128 bytes], 128-byte swizzle
-  static constexpr int STAGE = 2 * TILE;         // K, then V
-  static constexpr int RING = STAGES * STAGE;
+  static constexpr int SLOT = (SPLIT ? 1 : 2) * TILE;   // 8 KB
+  static constexpr int RING = SLOTS * SLOT;
   static constexpr int SMEM = WARPS * RING + 1024;   // and what aligns it
-  static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
+  static constexpr int CTAS = 2;                 // per SM
 };
 constexpr int kPagedSms = 148;
 constexpr int kPagedMinUnits = 2;                // of a range: what is in flight at once
@@ -93,8 +97,8 @@ constexpr int kPagedPairUnits = 2;               // what beginning and ending a 
 // Rows of a row tile: rounded up to 8, 16 or (d < 256) 32.
 __host__ __device__ inline int paged_row_tile(int d, int rows) { return rows <= 8 ? 8 : rows <= 16 || d == 256 ? 16 : 32; }
 // Warps that share one row tile's work.
-__host__ __device__ inline int paged_workers(int d, int row_tiles) {
-  const int ctas = kPagedSms * (d == 256 ? 1 : 2) / row_tiles;
+__host__ __device__ inline int paged_workers(int row_tiles) {
+  const int ctas = kPagedSms * 2 / row_tiles;
   return (ctas < 1 ? 1 : ctas) * 4;
 }
 
@@ -160,15 +164,15 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ long long before[C::THREADS + 1];
   __shared__ long long warp_sum[C::WARPS];
-  __shared__ uint64_t bars[C::WARPS * C::STAGES];  // a stage's bytes have arrived
+  __shared__ uint64_t bars[C::WARPS * C::SLOTS];   // a slot's bytes have arrived
   __shared__ uint32_t abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int worker = blockIdx.x * C::WARPS + warp, rt = blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge kernel may come up, and waits for the end
 
-  const uint32_t bar0 = smem_u32(bars + warp * C::STAGES);
+  const uint32_t bar0 = smem_u32(bars + warp * C::SLOTS);
   if (lane == 0) {
-    for (int st = 0; st < C::STAGES; ++st) mbar_init(bar0 + 8 * st, 1);
+    for (int st = 0; st < C::SLOTS; ++st) mbar_init(bar0 + 8 * st, 1);
     fence_mbar_init();
   }
   if (tid == 0) {
@@ -246,38 +250,40 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
       }
     }
   };
-  int load_stage = 0;
-  auto load_tile = [&]() {
-    if (in.unit < t1) {
-      const int g = in.tile * (KT / 8), want = g & ~31;
-      if (want != g0) {                            // KT / 8 divides 32: a tile's groups are in one look-up
-        if (g0 < 0 || want != g0 + 32) look_up(want);
-        pg = pg_next;
-        row_in = row_next;
-        g0 = want;
-        look_up(want + 32);
-      }
-      const uint32_t st = ring + load_stage * C::STAGE, bar = bar0 + 8 * load_stage;
-      if (lane == 0) mbar_expect_tx(bar, C::STAGE);
+  int load_slot = 0;
+  bool load_v = false;                             // SPLIT: V is next
+  auto load_next = [&]() {                         // the tiles of `in`, or (SPLIT) one of them, into the next slot
+    if (in.unit >= t1) return;
+    const int g = in.tile * (KT / 8), want = g & ~31;
+    if (want != g0) {                              // KT / 8 divides 32: a tile's groups are in one look-up
+      if (g0 < 0 || want != g0 + 32) look_up(want);
+      pg = pg_next;
+      row_in = row_next;
+      g0 = want;
+      look_up(want + 32);
+    }
+    const uint32_t to = ring + load_slot * C::SLOT, bar = bar0 + 8 * load_slot;
+    if (lane == 0) mbar_expect_tx(bar, C::SLOT);
 #pragma unroll 1
-      for (int key = 0; key < KT; key += a.box) {
-        const int p = __shfl_sync(0xffffffffu, pg, (g - g0) + key / 8), row = __shfl_sync(0xffffffffu, row_in, (g - g0) + key / 8);
-        if (lane == 0) {
-          tma_load_5d(st + key * C::PITCH, &tm_k, bar, 0, row, 0, in.h, p);
-          tma_load_5d(st + key * C::PITCH + C::TILE, &tm_v, bar, 0, row, 0, in.h, p);
-        }
+    for (int key = 0; key < KT; key += a.box) {
+      const int p = __shfl_sync(0xffffffffu, pg, (g - g0) + key / 8), row = __shfl_sync(0xffffffffu, row_in, (g - g0) + key / 8);
+      if (lane == 0) {
+        tma_load_5d(to + key * C::PITCH, C::SPLIT && load_v ? &tm_v : &tm_k, bar, 0, row, 0, in.h, p);
+        if constexpr (!C::SPLIT) tma_load_5d(to + C::TILE + key * C::PITCH, &tm_v, bar, 0, row, 0, in.h, p);
       }
-      ++in.unit;
-      if (++in.tile == in.tiles) {
-        if (in.unit + kPagedPairUnits < t1) {
-          const int b = in.b;
-          in.next_pair<KT>(a);
-          if (in.b != b) g0 = -1;
-        } else {
-          in.unit = t1;
-        }
+    }
+    load_slot = load_slot + 1 == C::SLOTS ? 0 : load_slot + 1;
+    load_v = C::SPLIT && !load_v;
+    if (load_v) return;
+    ++in.unit;
+    if (++in.tile == in.tiles) {
+      if (in.unit + kPagedPairUnits < t1) {
+        const int b = in.b;
+        in.next_pair<KT>(a);
+        if (in.b != b) g0 = -1;
+      } else {
+        in.unit = t1;
       }
-      load_stage = load_stage + 1 == C::STAGES ? 0 : load_stage + 1;
     }
   };
 
@@ -291,25 +297,25 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   const int my_row = rt * RM + lane, my_g = my_row / a.N, my_i = my_row - my_g * a.N;
   const bool my_real = lane < RM && my_row < a.rows;
   const long long q_row = my_real ? my_g * a.sq.h + my_i * a.sq.r : -1, o_row = my_g * a.so.h + my_i * a.so.r;
-  // Q goes through the stage that is loaded next, rows without a query as zeros.
+  // Q goes through the slot that is loaded next, a 16-row tile at a time, rows without a query as zeros.
   auto begin_pair = [&]() {
-    const uint32_t st = ring + load_stage * C::STAGE;
-    constexpr int CH = D / 8, RPI = 32 / CH;       // 16-byte chunks of a row; rows per warp copy
+    const uint32_t to = ring + load_slot * C::SLOT;
+    constexpr int CH = D / 8, RPI = 32 / CH, ROWS = C::HALF ? 8 : 16;   // 16-byte chunks of a row; rows per warp copy
     const int ch = lane % CH;
     const __nv_bfloat16* q = a.q + at.b * a.sq.b + static_cast<long long>(at.h) * a.group * a.sq.h + ch * 8;
-#pragma unroll 1
-    for (int r = 0; r < RM; r += RPI) {
-      const int rr = r + lane / CH;
-      const long long off = __shfl_sync(0xffffffffu, q_row, rr);
-      copy16(st + rr * C::PITCH + ((ch ^ (rr & 7)) << 4), off < 0 ? a.q : q + off, off >= 0);
-    }
-    copy_commit();
-    copy_wait<0>();
-    __syncwarp();
     const int row = (lane & 7) + (C::HALF ? 0 : ((lane >> 3) & 1) * 8), hi = C::HALF ? lane >> 3 : lane >> 4;
-    const uint32_t qa = st + row * C::PITCH + ((hi ^ (row & 7)) << 4);
+    const uint32_t qa = to + row * C::PITCH + ((hi ^ (row & 7)) << 4);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll 1
+      for (int r = 0; r < ROWS; r += RPI) {
+        const int rr = r + lane / CH;
+        const long long off = __shfl_sync(0xffffffffu, q_row, mt * 16 + rr);
+        copy16(to + rr * C::PITCH + ((ch ^ (rr & 7)) << 4), off < 0 ? a.q : q + off, off >= 0);
+      }
+      copy_commit();
+      copy_wait<0>();
+      __syncwarp();
       if constexpr (C::HALF) {                     // two k-steps at a time: chunks 4 x .. 4 x + 3
 #pragma unroll
         for (int k = 0; k < D / 16; k += 2) {
@@ -322,7 +328,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) ldsm4((qa ^ (32 * k)) + mt * 16 * C::PITCH, qf[mt][k]);
+        for (int k = 0; k < D / 16; ++k) ldsm4(qa ^ (32 * k), qf[mt][k]);
       }
 #pragma unroll
       for (int w = 0; w < RW; ++w) {
@@ -333,9 +339,10 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
       for (int n = 0; n < D / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.f;
+      __syncwarp();                                // everyone has its Q
     }
     fence_proxy_async_smem();
-    __syncwarp();                                  // everyone has its Q: the stage is free for TMA
+    __syncwarp();                                  // the slot is free for TMA
   };
   auto end_pair = [&](bool begins, bool ends) {    // of the pair's tiles this warp had the first, the last
     const bool whole = begins && ends;
@@ -378,49 +385,50 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   };
 
   // One copy of every step in the code: a launch runs each of them a few times only, and what it costs then is fetching
-  // the instructions (two more copies of load_tile and one of begin_pair took the shortest calls from 7 to 12-30 us).
-  bool fresh = true, begins = at.tile == 0;
-  int stage = 0;
-  uint32_t phase = 0;                              // bit of each stage: parity of its next arrival
+  // the instructions (two more copies of load_next and one of begin_pair took the shortest calls from 7 to 12-30 us).
+  bool fresh = true, begins = at.tile == 0, second = false;   // second (SPLIT): P is ready, V is next
+  int slot = 0;
+  uint32_t phase = 0;                              // bit of each slot: parity of its next arrival
   const WaitCtl ctl{&abort_flag, a.status, a.wait_limit_ns};
   // where key `key` of a tile lies, and the bytes between its 64-column pieces
   const int piece = a.box * 128;
   auto key_at = [&](int key) { return D == 64 ? key * 128 : key / a.box * (a.box * C::PITCH) + key % a.box * 128; };
   const int krow = (lane & 7) + ((lane >> 4) << 3), vrow = lane & 15;
   const uint32_t k_lane = key_at(krow) + ((((lane >> 3) & 1) ^ (krow & 7)) << 4);
-  const uint32_t v_lane = C::TILE + key_at(vrow) + (((lane >> 4) ^ (vrow & 7)) << 4);
+  const uint32_t v_lane = key_at(vrow) + (((lane >> 4) ^ (vrow & 7)) << 4);
+  uint32_t p[MT][NT / 2][4];                       // per 16 keys: keys 0 .. 7 (rows, rows + 8), then keys 8 .. 15
 #pragma unroll 1
-  for (int ahead = C::STAGES - 1;;) {              // tiles to load before the first is used
+  for (int ahead = C::SLOTS - 1;;) {               // tiles to load before the first is used
     if (ahead == 0) {
-      if (!mbar_wait_warp(bar0 + 8 * stage, (phase >> stage) & 1, ctl)) {   // (and everyone is done with the last tile)
-        // let the copies in flight land (bounded): every stage but the free one
+      if (!mbar_wait_warp(bar0 + 8 * slot, (phase >> slot) & 1, ctl)) {   // (and everyone is done with the last slot)
+        // let the copies in flight land (bounded): every slot but the free one
         if (lane == 0)
-          for (int st = 0; st < C::STAGES; ++st)
-            if (st != load_stage) mbar_wait_quiet(bar0 + 8 * st, (phase >> st) & 1, 200000000ull);
+          for (int st = 0; st < C::SLOTS; ++st)
+            if (st != load_slot) mbar_wait_quiet(bar0 + 8 * st, (phase >> st) & 1, 200000000ull);
         return;
       }
-      if (fresh) begin_pair();
+      if (fresh && !second) begin_pair();
     }
-    load_tile();
+    load_next();
     if (ahead > 0) {
       --ahead;
       continue;
     }
-    const uint32_t ks = ring + stage * C::STAGE;
-    phase ^= 1u << stage;
-    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-    // ---- S = Q K^T
-    float s[MT][NT][4];
+    const uint32_t here = ring + slot * C::SLOT, vt = here + (C::SPLIT ? 0 : C::TILE);
+    phase ^= 1u << slot;
+    slot = slot + 1 == C::SLOTS ? 0 : slot + 1;
+    if (!C::SPLIT || !second) {
+      // ---- S = Q K^T
+      float s[MT][NT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
-    {
+          for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t ka = (ks + k_lane + k / 4 * piece) ^ (32 * (k % 4));
+        const uint32_t ka = (here + k_lane + k / 4 * piece) ^ (32 * (k % 4));
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t kf[4];
@@ -434,102 +442,104 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
           }
         }
       }
-    }
-    // ---- masks: the tiles at the sequence's end
-    const int key0 = at.tile * KT + 2 * quad;
-    if ((at.tile + 1) * KT > at.len - (a.causal ? a.N - 1 : 0)) {
+      // ---- masks: the tiles at the sequence's end
+      if ((at.tile + 1) * KT > at.len - (a.causal ? a.N - 1 : 0)) {
+        const int key0 = at.tile * KT + 2 * quad;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int w = 0; w < RW; ++w) {
+            const int i = __shfl_sync(0xffffffffu, my_i, mt * 16 + w * 8 + (lane >> 2));
+            const int lim = a.causal ? at.len - a.N + i : at.len - 1;   // last key the row sees
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (key0 + 8 * n + e > lim) s[mt][n][2 * w + e] = -INFINITY;
+          }
+      }
+      // ---- online softmax
+      bool grew = false;
+      float alpha[MT][RW];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int w = 0; w < RW; ++w) {
-          const int i = __shfl_sync(0xffffffffu, my_i, mt * 16 + w * 8 + (lane >> 2));
-          const int lim = a.causal ? at.len - a.N + i : at.len - 1;   // last key the row sees
+          float top = fmaxf(s[mt][0][2 * w], s[mt][0][2 * w + 1]);
+#pragma unroll
+          for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[mt][n][2 * w], s[mt][n][2 * w + 1]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const bool grows = (top - m[mt][w]) * c2 > 8.0f;    // false while the row has seen no key
+          alpha[mt][w] = 1.0f;
+          if (grows) {
+            alpha[mt][w] = ex2_approx((m[mt][w] - top) * c2);
+            l[mt][w] *= alpha[mt][w];
+            m[mt][w] = top;
+            grew = true;
+          }
+          const float nb = m[mt][w] == -INFINITY ? 0.f : m[mt][w] * c2;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (key0 + 8 * n + e > lim) s[mt][n][2 * w + e] = -INFINITY;
+            for (int e = 0; e < 2; ++e) {
+              const float x = ex2_approx(fmaf(s[mt][n][2 * w + e], c2, -nb));
+              s[mt][n][2 * w + e] = x;
+              l[mt][w] += x;
+            }
         }
-      // values behind the end: P is 0 there, but 0 * NaN is not
-      const int left = at.len - at.tile * KT;
-      if (left < KT) {
-#pragma unroll 1
-        for (int e = lane; e < (KT - left) * (D / 8); e += 32) {
-          const int key = left + e / (D / 8), ch = e % (D / 8);
-          *reinterpret_cast<uint4*>(smem + warp * C::RING + (ks - ring) + C::TILE + key_at(key) + ch / 8 * piece + ch % 8 * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();                  // before TMA writes the stage again
-        __syncwarp();
+      if (!fresh && __any_sync(0xffffffffu, grew)) {   // on a pair's first tile there is nothing to rescale
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[mt][n][e] *= alpha[mt][C::HALF ? 0 : e >> 1];
       }
-    }
-    // ---- online softmax
-    bool grew = false;
-    float alpha[MT][RW];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int w = 0; w < RW; ++w) {
-        float top = fmaxf(s[mt][0][2 * w], s[mt][0][2 * w + 1]);
-#pragma unroll
-        for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[mt][n][2 * w], s[mt][n][2 * w + 1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool grows = (top - m[mt][w]) * c2 > 8.0f;      // false while the row has seen no key
-        alpha[mt][w] = 1.0f;
-        if (grows) {
-          alpha[mt][w] = ex2_approx((m[mt][w] - top) * c2);
-          l[mt][w] *= alpha[mt][w];
-          m[mt][w] = top;
-          grew = true;
-        }
-        const float nb = m[mt][w] == -INFINITY ? 0.f : m[mt][w] * c2;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float p = ex2_approx(fmaf(s[mt][n][2 * w + e], c2, -nb));
-            s[mt][n][2 * w + e] = p;
-            l[mt][w] += p;
-          }
-      }
-    if (!fresh && __any_sync(0xffffffffu, grew)) { // on a pair's first tile there is nothing to rescale
+      fresh = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mt][n][e] *= alpha[mt][C::HALF ? 0 : e >> 1];
+        for (int n = 0; n < NT; ++n) {
+          uint32_t* y = &p[mt][n / 2][2 * (n % 2)];
+          y[0] = pack_bf16x2(s[mt][n][0], s[mt][n][1]);
+          if constexpr (C::HALF) {
+            const float2 h = bf16x2_to_float2(y[0]);
+            y[1] = pack_bf16x2(s[mt][n][0] - h.x, s[mt][n][1] - h.y);
+          } else {
+            y[1] = pack_bf16x2(s[mt][n][2], s[mt][n][3]);
+          }
+        }
+      second = C::SPLIT;
+      if constexpr (C::SPLIT) continue;
     }
-    fresh = false;
+    second = false;
+    // values behind the end: P is 0 there, but 0 * NaN is not
+    const int left = at.len - at.tile * KT;
+    if (left < KT) {
+#pragma unroll 1
+      for (int e = lane; e < (KT - left) * (D / 8); e += 32) {
+        const int key = left + e / (D / 8), ch = e % (D / 8);
+        *reinterpret_cast<uint4*>(smem + (vt - smem_u32(smem)) + key_at(key) + ch / 8 * piece + ch % 8 * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();                    // before TMA writes the slot again
+      __syncwarp();
+    }
     // ---- O += P V
 #pragma unroll
-    for (int kk = 0; kk < NT / 2; ++kk) {
-      uint32_t p[MT][4];                           // keys 0 .. 7 of the 16 (rows, rows + 8), then keys 8 .. 15
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float* y = s[mt][2 * kk + x];
-          p[mt][2 * x] = pack_bf16x2(y[0], y[1]);
-          if constexpr (C::HALF) {
-            const float2 h = bf16x2_to_float2(p[mt][2 * x]);
-            p[mt][2 * x + 1] = pack_bf16x2(y[0] - h.x, y[1] - h.y);
-          } else {
-            p[mt][2 * x + 1] = pack_bf16x2(y[2], y[3]);
-          }
-        }
+    for (int kk = 0; kk < NT / 2; ++kk)
 #pragma unroll
       for (int n = 0; n < D / 8; n += 2) {
         uint32_t vf[4];
-        ldsm4_t(((ks + v_lane + n / 8 * piece) ^ (16 * (n % 8))) + 2048 * kk, vf);   // kk > 0: d = 64 only
+        ldsm4_t(((vt + v_lane + n / 8 * piece) ^ (16 * (n % 8))) + 2048 * kk, vf);   // kk > 0: d = 64 only
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16(acc[mt][n], p[mt][0], p[mt][1], p[mt][2], p[mt][3], vf[0], vf[1]);
-          mma_bf16(acc[mt][n + 1], p[mt][0], p[mt][1], p[mt][2], p[mt][3], vf[2], vf[3]);
+          const uint32_t* y = p[mt][kk];
+          mma_bf16(acc[mt][n], y[0], y[1], y[2], y[3], vf[0], vf[1]);
+          mma_bf16(acc[mt][n + 1], y[0], y[1], y[2], y[3], vf[2], vf[3]);
         }
       }
-    }
     const bool ends = at.tile + 1 == at.tiles, stop = at.unit + 1 + (ends ? kPagedPairUnits : 0) >= t1;
     if (ends || stop) end_pair(begins, ends);
     if (stop) break;

@@ -111,7 +111,7 @@ PagedPlan paged_plan(const fa_paged_layout& L) {
   // no more warps than the longest sequences that the table can hold give work to
   const long long units = ((1LL * L.max_pages * L.page_size + kt - 1) / kt + kPagedPairUnits) * L.B * L.H_kv;
   const long long ctas = (units + 4 * p.min_units - 1) / (4 * p.min_units);
-  p.workers = paged_workers(L.d, p.row_tiles);
+  p.workers = paged_workers(p.row_tiles);
   if (ctas < p.workers / 4) p.workers = static_cast<int>(ctas) * 4;
   const size_t parts = 2 * static_cast<size_t>(p.row_tiles) * p.workers * p.part_rows;
   p.o_bytes = round256(parts * L.d * 4);
