@@ -11,7 +11,9 @@
 //    all resident at once), whatever the lengths are.  A range covers the end of one
 //    pair, whole pairs, and the beginning of another; whole pairs are written out,
 //    the cut ones leave (max, sum, O) partials that the merge kernel joins.  The
-//    lengths are read on the device: a captured call follows them;
+//    lengths are read on the device: a captured call follows them.  When a table row
+//    holds a few tiles only, no pair is cut: there is nothing to plan and nothing to
+//    join, and the second launch falls away;
 //  * a warp fills its own ring of tiles by TMA, across the ends of pairs, and waits for
 //    nobody: no block barrier in the loop.  Beginning and ending a pair (its rows'
 //    loads, its outputs) counts as kPagedPairUnits tiles.  A box is 8, 16 or 32 keys of
@@ -49,6 +51,7 @@ struct PagedArgs {
   float scale_log2;
   int workers;                     // warps that share the work of one row tile
   int min_units;                   // least units of a warp's range
+  int whole_units;                 // short tables: units of every pair, none of which is cut; else 0
   int row_tiles;
   int part_rows;                   // rows of a partial
   float* part_o;                   // [row tile][worker][2][part_rows][D]
@@ -92,6 +95,11 @@ struct PagedCfg {
 };
 constexpr int kPagedSms = 148;
 constexpr int kPagedMinUnits = 2;                // of a range: what is in flight at once
+// Tiles of a table row up to which no pair is cut: 4, or 16 when there are pairs for half of the SMs' blocks.  One pair's
+// tiles one after the other take longer than in parts, but planning, partials and the second launch fall away.  Measured
+// uncut / cut: 16 x 8 pairs of 4 tiles (d 128) 6.7 / 10.4 us, of 8 tiles 10.0 / 10.6, of 12 tiles 13.1 / 11.0; 128 x 8 pairs
+// of 16 tiles 25.5 / 34.5; 128 x 4 pairs of 16 tiles (d 256) 35 / 44; 128 x 2 pairs of 16 tiles (24 rows) 31 / 23.
+__host__ __device__ inline int paged_whole_tiles(long long pairs) { return pairs >= 2 * 148 ? 16 : 4; }
 constexpr int kPagedPairUnits = 2;               // what beginning and ending a pair costs, in tiles
 
 // Rows of a row tile: rounded up to 8, 16 or (d < 256) 32.
@@ -142,10 +150,12 @@ struct PagedPlace {
     len = b < a.B ? paged_len(a, b) : 0;
     tiles = max(1, (len + KT - 1) / KT);
   }
+  // units of the line between this pair's tiles and the next one's
+  __device__ __forceinline__ int gap(const PagedArgs& a) const { return a.whole_units ? a.whole_units - tiles : kPagedPairUnits; }
   template <int KT>
   __device__ __forceinline__ void next_pair(const PagedArgs& a) {  // unit: already behind this pair's last tile
+    unit += gap(a);
     tile = 0;
-    unit += kPagedPairUnits;
     if (++h == a.H_kv) {
       h = 0;
       ++b;
@@ -181,52 +191,70 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   }
   if (tid == 0) abort_flag = 0u;                   // the barriers below come before every use
 
-  // ---- the line, of one head: thread t sums the units of sequences t q .. t q + q - 1
-  const int per_thread = (a.B + C::THREADS - 1) / C::THREADS;
-  {
-    long long mine = 0;
-    for (int b = tid * per_thread; b < min(a.B, (tid + 1) * per_thread); ++b)
-      mine += max(1, (paged_len(a, b) + KT - 1) / KT) + kPagedPairUnits;
-    long long x = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    long long base = 0;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
-    before[tid] = base + x - mine;
-    if (tid == C::THREADS - 1) before[C::THREADS] = base + x;
-    __syncthreads();
-  }
-  const long long total = before[C::THREADS] * a.H_kv;
-  const long long share = (total + a.workers - 1) / a.workers;
-  const long long range = share > a.min_units ? share : a.min_units;
-  const long long t0 = range * worker, t1 = t0 + range < total ? t0 + range : total;
-  if (t0 >= t1) return;
-
-  // ---- the first tile at or behind t0
+  long long t0, t1, range;
   PagedPlace in;                                   // the next tile to load
-  {
-    const long long s0 = t0 / a.H_kv;
-    int slot = 0;
-#pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) slot += __popc(__ballot_sync(0xffffffffu, before[32 * w + lane] <= s0));
-    in.b = (slot - 1) * per_thread;
-    long long base = before[slot - 1];
+  if (a.whole_units) {
+    // ---- every pair has its place in the line, whatever its length
+    const int pairs = a.B * a.H_kv, mine = (pairs + a.workers - 1) / a.workers;
+    range = static_cast<long long>(mine) * a.whole_units;
+    t0 = worker * range;
+    t1 = min(t0 + range, static_cast<long long>(pairs) * a.whole_units);
+    __syncthreads();                               // abort_flag
+    if (t0 >= t1) return;
+    const int first = worker * mine;               // below pairs
+    in.b = first / a.H_kv;
+    in.h = first - in.b * a.H_kv;
     in.enter<KT>(a);
-    while (base + in.tiles + kPagedPairUnits <= s0) {   // at most per_thread steps
-      base += in.tiles + kPagedPairUnits;
-      ++in.b;
-      in.enter<KT>(a);
+    in.tile = 0;
+    in.unit = t0 + kPagedPairUnits;
+  } else {
+    // ---- the line, of one head: thread t sums the units of sequences t q .. t q + q - 1
+    const int per_thread = (a.B + C::THREADS - 1) / C::THREADS;
+    {
+      long long mine = 0;
+      for (int b = tid * per_thread; b < min(a.B, (tid + 1) * per_thread); ++b)
+        mine += max(1, (paged_len(a, b) + KT - 1) / KT) + kPagedPairUnits;
+      long long x = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      long long base = 0;
+      for (int w = 0; w < warp; ++w) base += warp_sum[w];
+      before[tid] = base + x - mine;
+      if (tid == C::THREADS - 1) before[C::THREADS] = base + x;
+      __syncthreads();
     }
-    const long long rest = t0 - base * a.H_kv;     // of this sequence's H_kv (tiles + kPagedPairUnits)
-    const long long units = in.tiles + kPagedPairUnits;
-    in.h = static_cast<int>(rest / units);
-    const int u = static_cast<int>(rest - in.h * units) - kPagedPairUnits;
-    in.tile = max(0, u);
-    in.unit = t0 + in.tile - u;
+    const long long total = before[C::THREADS] * a.H_kv;
+    const long long share = (total + a.workers - 1) / a.workers;
+    range = share > a.min_units ? share : a.min_units;
+    t0 = range * worker;
+    t1 = min(t0 + range, total);
+    if (t0 >= t1) return;
+
+    // ---- the first tile at or behind t0
+    {
+      const long long s0 = t0 / a.H_kv;
+      int slot = 0;
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) slot += __popc(__ballot_sync(0xffffffffu, before[32 * w + lane] <= s0));
+      in.b = (slot - 1) * per_thread;
+      long long base = before[slot - 1];
+      in.enter<KT>(a);
+      while (base + in.tiles + kPagedPairUnits <= s0) {   // at most per_thread steps
+        base += in.tiles + kPagedPairUnits;
+        ++in.b;
+        in.enter<KT>(a);
+      }
+      const long long rest = t0 - base * a.H_kv;     // of this sequence's H_kv (tiles + kPagedPairUnits)
+      const long long units = in.tiles + kPagedPairUnits;
+      in.h = static_cast<int>(rest / units);
+      const int u = static_cast<int>(rest - in.h * units) - kPagedPairUnits;
+      in.tile = max(0, u);
+      in.unit = t0 + in.tile - u;
+    }
   }
   if (in.unit >= t1) return;
   PagedPlace at = in;                              // the next tile to use
@@ -277,7 +305,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     if (load_v) return;
     ++in.unit;
     if (++in.tile == in.tiles) {
-      if (in.unit + kPagedPairUnits < t1) {
+      if (in.unit + in.gap(a) < t1) {
         const int b = in.b;
         in.next_pair<KT>(a);
         if (in.b != b) g0 = -1;
@@ -378,7 +406,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
           }
         }
       }
-    if (begins && lane == 0) {
+    if (begins && !a.whole_units && lane == 0) {
       const int more = ends ? 0 : static_cast<int>((at.unit + at.tiles - 1 - at.tile) / range) - worker;
       a.meta[(static_cast<long long>(rt) * a.B + at.b) * a.H_kv + at.h] = make_int2(worker, more);
     }
@@ -540,7 +568,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
           mma_bf16(acc[mt][n + 1], y[0], y[1], y[2], y[3], vf[2], vf[3]);
         }
       }
-    const bool ends = at.tile + 1 == at.tiles, stop = at.unit + 1 + (ends ? kPagedPairUnits : 0) >= t1;
+    const bool ends = at.tile + 1 == at.tiles, stop = at.unit + 1 + (ends ? at.gap(a) : 0) >= t1;
     if (ends || stop) end_pair(begins, ends);
     if (stop) break;
     ++at.tile;

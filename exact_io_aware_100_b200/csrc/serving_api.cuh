@@ -95,9 +95,9 @@ fa_status check_decode(const fa_paged_layout& L) {
 
 // How a decode call is cut up, and where its workspace's parts lie.
 struct PagedPlan {
-  int rm, row_tiles, workers, part_rows, min_units;
-  size_t o_bytes, ml_bytes, meta_bytes;
-  size_t bytes() const { return o_bytes + ml_bytes + meta_bytes; }
+  int rm, row_tiles, workers, part_rows, min_units, whole_units;
+  size_t o_bytes, ml_bytes, meta_bytes;            // none is needed when no pair is cut
+  size_t bytes() const { return whole_units ? 256 : o_bytes + ml_bytes + meta_bytes; }
 };
 PagedPlan paged_plan(const fa_paged_layout& L) {
   PagedPlan p;
@@ -109,8 +109,10 @@ PagedPlan paged_plan(const fa_paged_layout& L) {
   const int kt = L.d == 64 ? 32 : 16;
   p.min_units = std::max(kPagedMinUnits, 2 * p.part_rows / kt);
   // no more warps than the longest sequences that the table can hold give work to
-  const long long units = ((1LL * L.max_pages * L.page_size + kt - 1) / kt + kPagedPairUnits) * L.B * L.H_kv;
-  const long long ctas = (units + 4 * p.min_units - 1) / (4 * p.min_units);
+  const long long most = (1LL * L.max_pages * L.page_size + kt - 1) / kt, pairs = 1LL * L.B * L.H_kv;
+  p.whole_units = most <= paged_whole_tiles(pairs) ? static_cast<int>(most) + kPagedPairUnits : 0;
+  const long long units = p.whole_units ? pairs : (most + kPagedPairUnits) * pairs, least = p.whole_units ? 1 : p.min_units;
+  const long long ctas = (units + 4 * least - 1) / (4 * least);
   p.workers = paged_workers(p.row_tiles);
   if (ctas < p.workers / 4) p.workers = static_cast<int>(ctas) * 4;
   const size_t parts = 2 * static_cast<size_t>(p.row_tiles) * p.workers * p.part_rows;
@@ -148,6 +150,7 @@ fa_status launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Paged
     *attr = true;
   }
   fa_paged_decode_kernel<D, RM><<<dim3(a.workers / C::WARPS, a.row_tiles), C::THREADS, C::SMEM, s>>>(tk, tv, a);
+  if (a.whole_units) return launched();
   // the merge: 8, 4, 2 or 1 warps to a row, as many as the GPU holds at once; launched while the first kernel runs
   const long long rows = 1LL * a.B * a.H * a.N;
   const int per_row = rows <= kPagedSms * 8 ? 8 : rows <= kPagedSms * 16 ? 4 : rows <= kPagedSms * 32 ? 2 : 1;
@@ -364,6 +367,7 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   a.row_tiles = plan.row_tiles;
   a.part_rows = plan.part_rows;
   a.min_units = plan.min_units;
+  a.whole_units = plan.whole_units;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + plan.o_bytes);
