@@ -428,6 +428,10 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 #pragma unroll 1
   for (int ahead = C::SLOTS - 1;;) {               // tiles to load before the first is used
     if (ahead == 0) {
+      if (fresh && !second) {                      // while the pair's first tile is on its way
+        __syncwarp();                              // everyone is done with the free slot
+        begin_pair();
+      }
       if (!mbar_wait_warp(bar0 + 8 * slot, (phase >> slot) & 1, ctl)) {   // (and everyone is done with the last slot)
         // let the copies in flight land (bounded): every slot but the free one
         if (lane == 0)
@@ -435,7 +439,6 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             if (st != load_slot) mbar_wait_quiet(bar0 + 8 * st, (phase >> st) & 1, 200000000ull);
         return;
       }
-      if (fresh && !second) begin_pair();
     }
     load_next();
     if (ahead > 0) {

@@ -173,6 +173,10 @@ bool pages_layout_ok(const fa_pages_layout* L) {
          (L->num_seqs == 1 || L->table_stride >= L->max_pages);
 }
 
+// Threads of a planning block: fewer warps take barriers faster, more take long lists in fewer steps.  48 forks and 48
+// extensions among 20000 pages: 10.3 + 5.6 us with 256 threads, 8.0 + 4.6 with 512, 9.0 + 5.5 with 1024.
+int pages_threads(int items) { return items <= 512 ? 512 : kPagesThreads; }
+
 // Workspace of the page calls: claim [S], snap [n], prefix [n], list [P], info [1].
 size_t pages_ws_bytes(const fa_pages_layout& L, int n) {
   return round256(4 * static_cast<size_t>(L.num_seqs)) + 2 * round256(4 * static_cast<size_t>(n)) +
@@ -407,7 +411,7 @@ fa_status fa_pages_extend(int32_t* page_table, int32_t* seq_lens, int32_t* refco
   a.seqs = seqs;
   a.arg = tokens;
   a.status = status;
-  fa_pages_extend_kernel<<<1, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  fa_pages_extend_kernel<<<1, pages_threads(n), 0, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
 
@@ -423,7 +427,7 @@ fa_status fa_pages_fork(int32_t* page_table, int32_t* seq_lens, int32_t* refcoun
   a.arg = dst;
   a.copies = copies;
   a.status = status;
-  fa_pages_fork_kernel<<<1, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  fa_pages_fork_kernel<<<1, pages_threads(n), 0, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
 
@@ -448,8 +452,8 @@ fa_status fa_pages_compact(int32_t* page_table, const int32_t* seq_lens, int32_t
   if (st != FA_OK) return st;
   a.copies = copies;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  fa_pages_plan_compact_kernel<<<1, kPagesThreads, 0, s>>>(a);
-  fa_pages_rename_kernel<<<(a.S + 3) / 4, 128, 0, s>>>(a);
+  fa_pages_plan_compact_kernel<<<1, pages_threads(a.P / kPagesPer), 0, s>>>(a);
+  if (1LL * a.S * a.M > kPagesRenameHere) fa_pages_rename_kernel<<<(a.S + 3) / 4, 128, 0, s>>>(a);
   return launched();
 }
 

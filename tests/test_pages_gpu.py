@@ -49,6 +49,7 @@ def _ok(code=0):
     (3, 20, 3, 4, [5, 0, 12], [0, 0, 2, -1, 3, 1, 1], [1, 1, 1, 1, 1, -2, 9]),   # repeated, full, out of range, negative
     (300, 20000, 70, 16, [], list(range(299, -1, -1)), [(i * 37) % 1100 for i in range(300)]),
     (1500, 40000, 3, 8, [], list(range(1500)), [i % 25 for i in range(1500)]),   # more requests than threads
+    (3000, 5000, 3, 8, [], list(range(2999, -1, -1)), [i % 25 for i in range(3000)]),   # lists beyond shared memory; pages run out
 ])
 def test_extend(S, P, M, page, lens, seqs, tokens):
     import exact_io_aware_100_b200 as fa
@@ -67,6 +68,7 @@ def test_extend(S, P, M, page, lens, seqs, tokens):
     (6, 6, 4, 16, [50, 16], [0, 0, 0, 1], [2, 3, 4, 5]),              # one page left for three copies; the last wants none
     (6, 30, 4, 16, [50, 16], [0, 2, 3, 0, 9, 0, -1, 4], [2, 3, 3, 1, 4, 6, 5, 4]),   # empty source, taken, range, itself
     (400, 9000, 40, 16, [(i * 53) % 640 for i in range(200)], [i // 2 for i in range(200)], list(range(200, 400))),
+    (5000, 9000, 2, 16, [(i * 7) % 32 for i in range(2500)], list(range(2500)), list(range(2500, 5000))),
 ])
 def test_fork(S, P, M, page, lens, src, dst):
     import exact_io_aware_100_b200 as fa
