@@ -178,7 +178,6 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   __shared__ uint32_t abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int worker = blockIdx.x * C::WARPS + warp, rt = blockIdx.y;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge kernel may come up, and waits for the end
 
   const uint32_t bar0 = smem_u32(bars + warp * C::SLOTS);
   if (lane == 0) {
@@ -190,6 +189,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     prefetch_tmap(&tm_v);
   }
   if (tid == 0) abort_flag = 0u;                   // the barriers below come before every use
+  after_previous_kernel();
 
   long long t0, t1, range;
   PagedPlace in;                                   // the next tile to load
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
   const unsigned rows = static_cast<unsigned>(a.B) * a.H * a.N;
   const unsigned row = blockIdx.x * (8u / per_row) + warp / per_row;
   const int sub = warp % per_row;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous_kernel();
   float acc[V];
   float m = -INFINITY, l = 0.f;
 #pragma unroll

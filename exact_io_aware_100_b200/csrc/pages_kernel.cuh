@@ -147,6 +147,7 @@ __device__ __forceinline__ void claim_sequences(const PagesArgs& a, Seq seq) {
 // Sequences grow by tokens and get the pages they need.  snap[i]: the pages wanted, -1 for a bad request.
 __global__ void __launch_bounds__(kPagesThreads) fa_pages_extend_kernel(PagesArgs a) {
   __shared__ PagesShared sh;
+  after_previous_kernel();
   use_shared(a, sh);
   const unsigned first = free_bits(a, threadIdx.x * kPagesPer);
   for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_extend_kernel(PagesArg
 // snap[i]: the source's length, -1 for a bad request.
 __global__ void __launch_bounds__(kPagesThreads) fa_pages_fork_kernel(PagesArgs a) {
   __shared__ PagesShared sh;
+  after_previous_kernel();
   use_shared(a, sh);
   const unsigned first = free_bits(a, threadIdx.x * kPagesPer);
   for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
@@ -238,6 +240,7 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_fork_kernel(PagesArgs 
 
 // Sequences become empty.  One warp per request; the first to take a sequence's length frees its pages.
 __global__ void __launch_bounds__(128) fa_pages_free_kernel(const PagesArgs a) {
+  after_previous_kernel();
   const int i = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= a.n) return;
   const int s = __ldg(a.seqs + i);
@@ -279,6 +282,7 @@ constexpr int kPagesRenameHere = 16384;
 
 // Ranks the pages in use and the holes among them; lists the moves; moves the reference counts.
 __global__ void __launch_bounds__(kPagesThreads) fa_pages_plan_compact_kernel(const PagesArgs a) {
+  after_previous_kernel();
   const unsigned first = free_bits(a, threadIdx.x * kPagesPer);
   int mine = 0, live;
   const int step = blockDim.x * kPagesPer;
@@ -323,6 +327,7 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_plan_compact_kernel(co
 
 // The page tables name the new places.  One warp per sequence.
 __global__ void __launch_bounds__(128) fa_pages_rename_kernel(const PagesArgs a) {
+  after_previous_kernel();
   const int s = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (s >= a.S) return;
   const int live = *a.info, len = a.lens[s];
@@ -349,6 +354,7 @@ constexpr int kPageCopyBytes = 16384;   // of a part: four 16-byte vectors in fl
 // list's rows team, team + teams, ...; its lanes look at 32 of them at once, so a list that is mostly empty costs one
 // read.  16 bytes at a time, a thread has a fixed column.
 __global__ void __launch_bounds__(256) fa_pages_copy_kernel(const PageCopyArgs a) {
+  after_previous_kernel();
   const int lane = threadIdx.x & 31;
   const int parts = 2 * a.H_kv * a.row_parts, teams = gridDim.x / parts;
   const int team = blockIdx.x / parts, part = blockIdx.x - team * parts;

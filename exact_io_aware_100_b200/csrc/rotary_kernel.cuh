@@ -144,6 +144,7 @@ __device__ __forceinline__ float2 rot_turn(float xa, float xb, float2 cs) {
 // p of the r / 2, or column r + (p - r / 2) of those that are copied.
 template <typename T, bool APPEND>
 __global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a, int interleaved, int heads_per) {
+  after_previous_kernel();
   const int half = a.r / 2, per = half + a.d - a.r;
   const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   const long long t = idx / per;
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(kRotThreads) fa_rotary_vec_kernel(const __grid
   using R = RotVec<T, V>;
   using Word = typename R::Word;
   extern __shared__ __align__(16) uint8_t rot_smem[];
+  after_previous_kernel();
   Word* buf = reinterpret_cast<Word*>(rot_smem) + threadIdx.x;   // [head][vector][thread]
   const int per = a.d / (2 * V), turning = a.r / (2 * V);      // items of a token, of which these turn
   const long long idx = static_cast<long long>(blockIdx.x) * kRotThreads + threadIdx.x;
