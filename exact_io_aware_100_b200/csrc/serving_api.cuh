@@ -90,7 +90,7 @@ fa_status launch_rotary(const RotArgs& a, int interleaved, DevState* ds, cudaStr
 fa_status check_paged(const fa_paged_layout& L) {
   if (L.B < 1 || L.H_kv < 1 || L.num_pages < 1 || L.max_pages < 1 || L.page_size < 1) return FA_ERR_INVALID;
   if (L.d != 64 && L.d != 128 && L.d != 256) return FA_ERR_UNSUPPORTED;
-  if (L.page_size % 8 != 0 || L.page_size > 65536 || 1LL * L.max_pages * L.page_size >= (1LL << 31) ||
+  if (L.page_size % 8 != 0 || L.page_size > 65536 || 1LL * L.max_pages * L.page_size > (1LL << 30) ||
       L.num_pages >= (1 << 30) || (L.B > 1 && L.table_stride < L.max_pages))
     return FA_ERR_INVALID;
   if (!strides_ok(L.k_pages, L.page_size, L.H_kv, L.num_pages) || !strides_ok(L.v_pages, L.page_size, L.H_kv, L.num_pages))
@@ -234,7 +234,7 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
                     fa_dtype dtype, fa_stream_t stream) {
   if (layout == nullptr) return FA_ERR_INVALID;
   const fa_rotary_layout& L = *layout;
-  if (L.B < 1 || L.H < 1 || L.H_kv < 0 || L.H >= (1 << 18) || L.H_kv >= (1 << 18) || L.N < 0 || L.d < 1 || L.d > 1024 || L.rotary_dim < 0 || L.rotary_dim > L.d ||
+  if (L.B < 1 || L.H < 1 || L.H_kv < 0 || L.H >= (1 << 16) || L.H_kv >= (1 << 16) || L.N < 0 || L.d < 1 || L.d > 1024 || L.rotary_dim < 0 || L.rotary_dim > L.d ||
       L.rotary_dim % 2 != 0 || 1LL * L.B * L.N >= (1LL << 31) || !std::isfinite(magnitude) ||
       !out_strides_ok(L.q_out, L.B, L.H, L.N) || (L.H_kv > 0 && !out_strides_ok(L.k_out, L.B, L.H_kv, L.N)))
     return FA_ERR_INVALID;
@@ -282,7 +282,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
   if (st != FA_OK) return st;
   const bool pk = L.cu_seqlens != nullptr;
   const long long tokens = pk ? L.total : 1LL * L.B * L.N;
-  if ((pk ? L.total : L.N) < 0 || tokens >= (1LL << 31) || (q != nullptr && (L.H < 1 || L.H >= (1 << 18))) || L.H_kv >= (1 << 18) || !std::isfinite(magnitude) ||
+  if ((pk ? L.total : L.N) < 0 || tokens >= (1LL << 31) || (q != nullptr && (L.H < 1 || L.H >= (1 << 16))) || L.H_kv >= (1 << 16) || !std::isfinite(magnitude) ||
       (freqs != nullptr && (L.rotary_dim < 0 || L.rotary_dim > L.d || L.rotary_dim % 2 != 0)))
     return FA_ERR_INVALID;
   if (tokens == 0) return FA_OK;

@@ -260,7 +260,7 @@ size_t fa_decode_workspace_size(int B, int H, int H_kv, int Lq, int Nk, int d);
  *  point as fractions of a turn, exact for every int32 position; products and
  *  sums are 32-bit, one rounding to dtype at the end.
  * rotary_dim even, 0 <= rotary_dim <= d <= 1024 (FA_ERR_INVALID; d need not be
- * a multiple of 8).  B, H >= 1, N >= 0; B * N < 2^31; H, H_kv < 2^18.  Pointers are aligned to the element size
+ * a multiple of 8).  B, H >= 1, N >= 0; B * N < 2^31; H, H_kv < 2^16.  Pointers are aligned to the element size
  * (FA_ERR_ALIGN).  Pointers and strides that are multiples of 16 bytes, with rotary_dim and d multiples of two such
  * vectors, take the fast path (of 8 bytes in bf16: a little slower).
  */
@@ -283,7 +283,7 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
  * page_table[b * table_stride + j / page_size].  page_table and seq_lens are
  * DEVICE int32; the entries of a row behind its last page are never used.
  * d in {64, 128, 256} (FA_ERR_UNSUPPORTED); page_size a multiple of 8, at most
- * 65536, and max_pages (entries of a table row) >= 1 with max_pages * page_size < 2^31
+ * 65536, and max_pages (entries of a table row) >= 1 with max_pages * page_size <= 2^30
  * (FA_ERR_INVALID).  A sequence length that is negative or beyond max_pages *
  * page_size, and a page number outside 0 .. num_pages - 1, are reported by
  * fa_get_device_status as FA_ERR_INVALID; no memory outside the tensors is
@@ -314,7 +314,7 @@ typedef struct {
  * sequence shorter than n: padding) is not written and its row of o is zero.
  * A packed row outside every sequence is not written either; its row of o is
  * zero, or what it was when o is q.  Two sequences must not receive tokens
- * on the same page.  H is only used with q.
+ * on the same page.  H is only used with q; H, H_kv < 2^16.
  */
 fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, void* k_pages, void* v_pages,
                           const int32_t* page_table, const int32_t* seq_lens, const double* freqs,

@@ -319,3 +319,94 @@ def test_decode_two_streams_and_a_graph():
         ro, rl = fa.paged_decode(q, kp, vp, table, sl)
         assert torch.equal(o, ro) and torch.equal(lse, rl)
     assert fa.fa_get_device_status() == fa.FA_OK
+
+
+def _reference(q, kp, vp, table, lens, causal, scale):
+    """Float64 attention of the gathered cache, one sequence at a time, on the device."""
+    import torch
+    B, H, N, d = q.shape
+    H_kv, page = kp.shape[1:3]
+    o, lse = torch.zeros(q.shape, dtype=torch.float64, device="cuda"), torch.full((B, H, N), -float("inf"), dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        rows = table[b, :-(-n // page)].long()
+        k, v = (p[rows].transpose(0, 1).reshape(H_kv, -1, d)[:, :n].double().repeat_interleave(H // H_kv, 0) for p in (kp, vp))
+        x = q[b].double() @ k.transpose(1, 2) * scale
+        if causal:
+            hidden = torch.arange(n, device="cuda")[None, :] > (n - N + torch.arange(N, device="cuda"))[:, None]
+            x.masked_fill_(hidden, -float("inf"))
+        lse[b] = torch.logsumexp(x, -1)
+        top = lse[b].masked_fill(lse[b] == -float("inf"), 0.0)
+        o[b] = (x - top[..., None]).exp() @ v
+    return o, lse
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_decode_anywhere_in_the_range(seed):
+    """Sizes, lengths and layouts at random: cut and uncut pairs, every row tile, every box, idle and tiny sequences."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    rng = np.random.default_rng(9000 + seed)
+    pick = lambda *x: x[int(rng.integers(len(x)))]  # noqa: E731
+    d, page, H_kv, group, N = pick(64, 128, 256), pick(8, 16, 24, 32, 48, 64, 128), pick(1, 2, 5, 8), pick(1, 2, 3, 4, 8), pick(1, 1, 2, 4, 9)
+    B = int(np.exp(rng.uniform(0, np.log(160))))
+    most = int(np.exp(rng.uniform(0, np.log(min(20000, 6_000_000 // (B * H_kv * d) * 8 + 2)))))
+    lens = [most] + [int(np.exp(rng.uniform(0, np.log(most + 0.99)))) - pick(0, 0, 1) for _ in range(B - 1)]
+    P = sum(-(-n // page) for n in lens) + 3
+    kp, vp = _cache(P, H_kv, page, d, pick(True, False), fill=NAN)
+    table, sl = _table(lens, page, P, M=-(-most // page) + pick(0, 0, 7), seed=seed)
+    for p in (kp, vp):                               # values at the positions in use, NaN everywhere else
+        for b, n in enumerate(lens):
+            if n:
+                rows = table[b, :-(-n // page)].long()
+                x = torch.full((len(rows) * page, H_kv, d), NAN, device="cuda")
+                x[:n] = torch.randn(n, H_kv, d, device="cuda")
+                p[rows] = x.view(len(rows), page, H_kv, d).transpose(1, 2).bfloat16()
+    q = torch.randn(B, N, H_kv * group, d, device="cuda").bfloat16().transpose(1, 2)
+    causal, scale = pick(True, False), pick(None, 0.2)
+    o, lse = fa.paged_decode(q, kp, vp, table, sl, causal, scale)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    ro, rl = _reference(q, kp, vp, table, lens, causal, 1 / np.sqrt(d) if scale is None else scale)
+    assert_close("O", to_f64(o), ro.cpu().numpy(), scale_max_abs=True)
+    rl, got = rl.cpu().numpy(), to_f64(lse)
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(got), empty) and not np.isnan(got).any()
+    assert (np.abs(got[~empty] - rl[~empty]) <= 1e-5 * np.maximum(1, np.abs(rl[~empty]))).all()
+    assert not to_f64(o)[empty].any()
+
+
+def test_calls_from_several_threads():
+    import threading
+
+    import torch
+    import exact_io_aware_100_b200 as fa
+    page, lens = 16, [3000, 50]
+    P = 200
+    kp, vp = _cache(P, 2, page, 128, True, fill=0.0)
+    kp.copy_(torch.randn(kp.shape, device="cuda"))
+    vp.copy_(torch.randn(vp.shape, device="cuda"))
+    table, sl = _table(lens, page, P)
+    q = torch.randn(2, 8, 1, 128, device="cuda").bfloat16()
+    freqs, _ = fa.rotary_frequencies(128)
+    want, turned = fa.paged_decode(q, kp, vp, table, sl), fa.rotary(q, None, freqs)[0]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(50):
+                o, lse = fa.paged_decode(q, kp, vp, table, sl)
+                y, _ = fa.rotary(q, None, freqs)
+                stream.synchronize()
+                if not (torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(y, turned)):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and fa.fa_get_device_status() == fa.FA_OK

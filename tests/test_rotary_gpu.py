@@ -162,3 +162,40 @@ def test_rotary_stream_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(out[0], fa.rotary(q, None, freqs)[0])
     assert (back[0].float() - q.float()).abs().max() < 0.06       # a turn there and back: two roundings of |x| < 6
+
+
+@pytest.mark.parametrize("H,H_kv,N,d,r", [(40000, 20000, 2, 16, 16), (1, 0, 300000, 16, 8), (65535, 0, 1, 8, 8)])
+def test_rotary_many_heads_or_rows(H, H_kv, N, d, r):
+    import torch
+    import exact_io_aware_100_b200 as fa
+    freqs, _ = fa.rotary_frequencies(r)
+    q = torch.randn(1, H, N, d, device="cuda").bfloat16()
+    k = torch.randn(1, H_kv, N, d, device="cuda").bfloat16() if H_kv else None
+    y, yk = fa.rotary(q, k, freqs)
+    at = [0, H // 2, H - 1]
+    rows = [0, N // 2, N - 1]
+    _check(y[:, at][:, :, rows], to_f64(q[:, at][:, :, rows]), np.asarray(rows), freqs.cpu().numpy(), 1.0, False, False, "bf16")
+    if H_kv:
+        _check(yk[:, -2:], to_f64(k[:, -2:]), np.arange(N), freqs.cpu().numpy(), 1.0, False, False, "bf16")
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_gradient_is_the_transpose(interleaved):
+    """<dy, f(x)> = <f^T(dy), x> in float32, and differences: f is linear, so f(x + h e) - f(x) = h f(e)."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    freqs, _ = fa.rotary_frequencies(48)
+    x, dy = (torch.randn(2, 3, 17, 64, device="cuda") for _ in range(2))
+    pos = torch.randint(0, 5000, (2, 17), dtype=torch.int32, device="cuda")
+    y, _ = fa.rotary(x, None, freqs, pos, interleaved, 1.3)
+    dx, _ = fa.rotary_backward(dy, None, freqs, pos, interleaved, 1.3)
+    a, b = (dy.double() * y.double()).sum(), (dx.double() * x.double()).sum()
+    # 6528 products of size about 1.3, each good to 1e-6 (the bound above) of 1.3 (|x_a| + |x_b|) |dy|
+    assert abs(float(a - b)) <= 6528 * 1e-6 * 1.3 * 8
+    h = 0.5
+    for col in (0, 1, 24, 47, 50):
+        e = torch.zeros_like(x)
+        e[..., col] = h
+        # two outputs of up to 8, each good to 1e-6 of |x_a| + |x_b| < 10, in two columns, times |dy| < 5, over h
+        step = fa.rotary(x + e, None, freqs, pos, interleaved, 1.3)[0].double() - y.double()
+        assert (((step * dy.double()).sum(-1) / h - dx[..., col].double()).abs() <= 4e-4).all()

@@ -57,6 +57,7 @@ def test_structs_match_the_header(tmp_path):
 @pytest.mark.parametrize("over,code", [
     (dict(B=0), INVALID), (dict(H=0), INVALID), (dict(H_kv=-1), INVALID), (dict(N=-1), INVALID), (dict(d=0), INVALID),
     (dict(d=1025), INVALID), (dict(rotary_dim=63), INVALID), (dict(rotary_dim=66), INVALID), (dict(rotary_dim=-2), INVALID),
+    (dict(H=1 << 16), INVALID), (dict(H_kv=1 << 16), INVALID),
     (dict(B=1 << 20, N=1 << 12), INVALID), (dict(q_out_row=0), INVALID), (dict(k_out_head=-64), INVALID), (dict(N=0), OK),
 ])
 def test_rotary_refuses(lib, over, code):
@@ -82,7 +83,8 @@ def test_rotary_refuses_pointers_types_and_magnitude(lib):
 CACHE = [
     (dict(B=0), INVALID), (dict(H_kv=0), INVALID), (dict(num_pages=0), INVALID), (dict(max_pages=0), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(page_size=12), INVALID), (dict(page_size=0), INVALID), (dict(page_size=65544), INVALID),
-    (dict(max_pages=1 << 28), INVALID), (dict(table_stride=3), INVALID), (dict(k_pages_row=60), ALIGN),
+    (dict(max_pages=1 << 28), INVALID), (dict(max_pages=(1 << 26) + 1, table_stride=1 << 27), INVALID),
+    (dict(table_stride=3), INVALID), (dict(k_pages_row=60), ALIGN),
     (dict(v_pages_head=0), ALIGN), (dict(k_pages_batch=-64), ALIGN),
 ]
 
@@ -111,7 +113,7 @@ def test_append_refuses_pointers(lib):
 
 @pytest.mark.parametrize("over,code", CACHE + [
     (dict(N=0), INVALID), (dict(H=5), INVALID), (dict(H=0), INVALID), (dict(q_head=68), ALIGN), (dict(o_batch=0), ALIGN),
-    (dict(B=1 << 20, H=1 << 12), INVALID),
+    (dict(B=1 << 20, H=1 << 12), INVALID), (dict(B=1, N=1 << 18), INVALID),
 ])
 def test_decode_refuses(lib, over, code):
     L = paged_layout(**over)
