@@ -100,6 +100,7 @@ constexpr int kPagedMinUnits = 2;                // of a range: what is in fligh
 // uncut / cut: 16 x 8 pairs of 4 tiles (d 128) 6.7 / 10.4 us, of 8 tiles 10.0 / 10.6, of 12 tiles 13.1 / 11.0; 128 x 8 pairs
 // of 16 tiles 25.5 / 34.5; 128 x 4 pairs of 16 tiles (d 256) 35 / 44; 128 x 2 pairs of 16 tiles (24 rows) 31 / 23.
 __host__ __device__ inline int paged_whole_tiles(long long pairs) { return pairs >= 2 * 148 ? 16 : 4; }
+constexpr int kPagedTeam = 32;
 constexpr int kPagedPairUnits = 2;               // what beginning and ending a pair costs, in tiles
 
 // Rows of a row tile: rounded up to 8, 16 or (d < 256) 32.
@@ -176,6 +177,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   __shared__ long long warp_sum[C::WARPS];
   __shared__ uint64_t bars[C::WARPS * C::SLOTS];   // a slot's bytes have arrived
   __shared__ uint32_t abort_flag;
+  __shared__ float2 team_ml[C::WARPS * RM];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int worker = blockIdx.x * C::WARPS + warp, rt = blockIdx.y;
 
@@ -257,6 +259,12 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     }
   }
   if (in.unit >= t1) return;
+  // Do the block's four ranges lie inside one pair, and is it cut into kPagedTeam ranges at least?  (The same answer in all
+  // four warps.)  Then they leave one partial: 33 MB of cache in 4 pairs (d 256) 23.7 -> 21 us with the merge.  With fewer
+  // ranges the block's own joining costs more than it saves, and with 32 rows it takes registers that the loop needs.
+  const long long tile0 = in.unit - in.tile, block0 = range * C::WARPS * blockIdx.x;
+  const bool team = RM <= 16 && !a.whole_units && block0 >= tile0 && block0 + range * C::WARPS <= tile0 + in.tiles &&
+                    in.tiles >= kPagedTeam * range;
   PagedPlace at = in;                              // the next tile to use
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
 
@@ -390,7 +398,8 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
           const float top = m[mt][w] == -INFINITY ? -INFINITY : m[mt][w] * c2;
           const float f = !whole ? 1.0f : sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
           char* to = whole ? reinterpret_cast<char*>(o + off)
-                           : reinterpret_cast<char*>(a.part_o + (slot + rr) * D + 2 * quad);
+                     : team ? reinterpret_cast<char*>(reinterpret_cast<float*>(smem + warp * C::RING) + rr * D + 2 * quad)
+                            : reinterpret_cast<char*>(a.part_o + (slot + rr) * D + 2 * quad);
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) {
             const float x = f * (C::HALF ? acc[mt][n][0] + acc[mt][n][2] : acc[mt][n][2 * w]);
@@ -402,7 +411,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             if (whole)
               a.lse[head0 * a.N + rt * RM + rr] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
             else
-              a.part_ml[slot + rr] = make_float2(top, sum);
+              (team ? team_ml + warp * RM : a.part_ml + slot)[rr] = make_float2(top, sum);
           }
         }
       }
@@ -437,6 +446,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         if (lane == 0)
           for (int st = 0; st < C::SLOTS; ++st)
             if (st != load_slot) mbar_wait_quiet(bar0 + 8 * st, (phase >> st) & 1, 200000000ull);
+        if (team) named_bar_and(1, C::THREADS, false);
         return;
       }
     }
@@ -581,6 +591,39 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
       fresh = begins = true;
     }
   }
+  if (!team || !named_bar_and(1, C::THREADS, true)) return;
+  // ---- the block's four partials become one, in the slot of its first warp; the others' slots hold nothing
+  const int head = blockIdx.x * C::WARPS;
+  for (int rr = warp; rr < min(RM, a.rows - rt * RM); rr += C::WARPS) {
+    float2 ml[C::WARPS];
+    float top = -INFINITY, sum = 0.f, w[C::WARPS];
+#pragma unroll
+    for (int x = 0; x < C::WARPS; ++x) {
+      ml[x] = team_ml[x * RM + rr];
+      top = fmaxf(top, ml[x].x);
+    }
+#pragma unroll
+    for (int x = 0; x < C::WARPS; ++x) {
+      w[x] = top == -INFINITY ? 1.f : exp2f(ml[x].x - top);
+      sum = fmaf(w[x], ml[x].y, sum);
+    }
+    auto slot_of = [&](int x) {
+      return ((static_cast<long long>(rt) * a.workers + head + x) * 2 + (x == 0 && block0 == tile0 ? 1 : 0)) * a.part_rows + rr;
+    };
+    if (lane < C::WARPS) a.part_ml[slot_of(lane)] = lane == 0 ? make_float2(top, sum) : make_float2(-INFINITY, 0.f);
+    float* to = a.part_o + slot_of(0) * D;
+#pragma unroll
+    for (int e = 2 * lane; e < D; e += 64) {
+      float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < C::WARPS; ++x) {
+        const float2 y = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(smem + x * C::RING) + rr * D + e);
+        z.x = fmaf(w[x], y.x, z.x);
+        z.y = fmaf(w[x], y.y, z.y);
+      }
+      *reinterpret_cast<float2*>(to + e) = z;
+    }
+  }
 }
 
 // Joins the partials of the pairs that several warps shared.  `per_row` warps (1, 2, 4 or 8) take a query row: a lane
@@ -591,6 +634,7 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
   auto col = [](int lane, int e) { return e / W * 32 * W + W * lane + e % W; };
   __shared__ float so[8][D];
   __shared__ float2 sml[8];
+  __shared__ int2 list[8][32];                     // partial, weight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned rows = static_cast<unsigned>(a.B) * a.H * a.N;
   const unsigned row = blockIdx.x * (8u / per_row) + warp / per_row;
@@ -628,11 +672,16 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
       m = mn;
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] *= old;
-      const int left = more - j0 - sub, cnt = left < 0 ? 0 : min(32, left / per_row + 1);
+      // those that hold anything, in order (most of a long pair's are empty: a block leaves one)
+      const unsigned there = __ballot_sync(0xffffffffu, !(w == 0.f));
+      __syncwarp();                                // the last round's list has been read
+      if (!(w == 0.f)) list[warp][__popc(there & ((1u << lane) - 1))] = make_int2(mine, __float_as_int(w));
+      __syncwarp();
+      const int cnt = __popc(there);
 #pragma unroll 8
       for (int j = 0; j < cnt; ++j) {
-        const int p = j0 + sub + j * per_row;
-        const float f = __shfl_sync(0xffffffffu, w, j);
+        const int p = list[warp][j].x;
+        const float f = __int_as_float(list[warp][j].y);
         const float* src = a.part_o + (first + (2LL * p + (p == 0 ? 1 : 0)) * a.part_rows) * D;
         struct __align__(4 * W) Piece { float x[W]; };
 #pragma unroll
