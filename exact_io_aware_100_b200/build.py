@@ -1,4 +1,4 @@
-"""Build libfa.so (sm_100a) in-tree with nvcc.
+"""Build libfa.so (sm_100a) in-tree with nvcc, and the serving operators' binding _serving.so with g++.
 
 Usage: python -m exact_io_aware_100_b200.build [--verbose]
 """
