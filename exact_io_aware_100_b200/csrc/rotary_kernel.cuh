@@ -221,8 +221,8 @@ __device__ __forceinline__ void rot_fetch(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// The vector path: aligned rows whose turned columns, and the others, fall into whole pairs of vectors of V elements (r
-// and d multiples of 2 V).  A thread takes two vectors of a token in up to kRotHeads heads: it asks for all of them
+// The vector path: aligned rows whose turned columns fall into whole pairs of vectors of V elements (half layout: r a
+// multiple of 2 V), or into whole vectors (interleaved: of V); d a multiple of 2 V.  A thread takes two vectors of a token in up to kRotHeads heads: it asks for all of them
 // (through shared memory, where they cost no registers: 32 KB a block, up to 224 KB an SM in flight), forms the angles
 // meanwhile, once for all heads, and turns and writes head by head.  It reads what it fetched itself: no barrier.
 // Training shape (2 x 40 heads x 8192 x 128, forward and backward): 109 us with 4 heads, 110 with 6, 112 with 8; 120
@@ -241,9 +241,12 @@ __global__ void __launch_bounds__(kRotThreads) fa_rotary_vec_kernel(const __grid
   if (t >= a.tokens) return;
   const int p = static_cast<int>(idx - t * per);
   const RotToken tk = rot_token<APPEND>(a, t);
-  const bool turn = p < turning;
-  // columns of the two vectors: half of the turned (or copied) columns apart, so that a warp's accesses are contiguous
-  const int ca = turn ? V * p : a.r + V * (p - turning), cb = ca + (turn ? a.r : a.d - a.r) / 2;
+  // columns of the two vectors, far apart, so that a warp's accesses are contiguous: the pairs of the half layout, or
+  // (interleaved) any two
+  const bool turn = !INTER && p < turning;
+  const int ca = turn || INTER ? V * p : a.r + V * (p - turning);
+  const int cb = ca + (turn ? a.r : INTER ? a.d : a.d - a.r) / 2;
+  const bool turn_a = INTER ? ca < a.r : turn, turn_b = INTER ? cb < a.r : turn;
   const bool pad = APPEND && (tk.skip || tk.page < 0);
   const int heads = pad ? (tk.skip && a.qo == a.q ? 0 : a.H) : a.H + (APPEND ? 2 : 1) * a.H_kv;
   const int h0 = blockIdx.y * heads_per, h1 = min(heads, h0 + heads_per);
@@ -263,20 +266,19 @@ __global__ void __launch_bounds__(kRotThreads) fa_rotary_vec_kernel(const __grid
       rot_fetch<sizeof(Word)>(buf + (2 * u + 1) * kRotThreads, x + cb);
     }
   float2 cs[V];                    // half layout: of column ca + e; interleaved: the pairs of one vector, then of the other
-  if (turn) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+  for (int e = 0; e < V; ++e)
+    if (e < V / 2 ? turn_a : turn_b) {
       const int pair = INTER ? (e < V / 2 ? ca : cb - V) / 2 + e : ca + e;
       cs[e] = rot_cos_sin(__ldg(a.freqs + pair), tk.pos, a.magnitude, a.inverse);
     }
-  }
   asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
   for (int h = h0; h < h1; ++h, buf += 2 * kRotThreads) {
     const RotHead r = rot_head<T, APPEND>(a, tk, h);
     T* y = static_cast<T*>(r.dst);
     Word va = buf[0], vb = buf[kRotThreads];
-    if (turn && r.turned) {
+    if (r.turned && (turn_a || turn_b)) {
       float xa[V], xb[V];
       R::unpack(va, xa);
       R::unpack(vb, xb);
@@ -284,12 +286,14 @@ __global__ void __launch_bounds__(kRotThreads) fa_rotary_vec_kernel(const __grid
       for (int e = 0; e < V; ++e) {
         float& fa = INTER ? (e < V / 2 ? xa[2 * e] : xb[2 * e - V]) : xa[e];
         float& fb = INTER ? (e < V / 2 ? xa[2 * e + 1] : xb[2 * e + 1 - V]) : xb[e];
-        const float2 z = rot_turn(fa, fb, cs[e]);
-        fa = z.x;
-        fb = z.y;
+        if (e < V / 2 ? turn_a : turn_b) {
+          const float2 z = rot_turn(fa, fb, cs[e]);
+          fa = z.x;
+          fb = z.y;
+        }
       }
-      va = R::pack(xa);
-      vb = R::pack(xb);
+      if (turn_a) va = R::pack(xa);
+      if (turn_b) vb = R::pack(xb);
     }
     *reinterpret_cast<Word*>(y + ca) = va;
     *reinterpret_cast<Word*>(y + cb) = vb;

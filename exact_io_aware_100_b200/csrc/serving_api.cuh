@@ -67,7 +67,7 @@ fa_status launch_rotary(const RotArgs& a, int interleaved, DevState* ds, cudaStr
   const int rows = APPEND && a.cu != nullptr ? a.total : a.N, nb = APPEND && a.cu != nullptr ? 1 : a.B;
   auto fits = [&](int v) {
     auto rows_ok = [&](const void* p, const Strides& st, int h) { return vec_rows(p, st, nb, h, rows, v * es, es); };
-    return a.d % (2 * v) == 0 && a.r % (2 * v) == 0 && (a.H == 0 || (rows_ok(a.q, a.sq, a.H) && rows_ok(a.qo, a.sqo, a.H))) &&
+    return a.d % (2 * v) == 0 && a.r % (interleaved ? v : 2 * v) == 0 && (a.H == 0 || (rows_ok(a.q, a.sq, a.H) && rows_ok(a.qo, a.sqo, a.H))) &&
            (a.H_kv == 0 || APPEND || (rows_ok(a.k, a.sk, a.H_kv) && rows_ok(a.ko, a.sko, a.H_kv)));
   };
   const int v = fits(V) ? V : es == 2 && fits(4) ? 4 : 0;

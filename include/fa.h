@@ -262,7 +262,7 @@ size_t fa_decode_workspace_size(int B, int H, int H_kv, int Lq, int Nk, int d);
  * rotary_dim even, 0 <= rotary_dim <= d <= 1024 (FA_ERR_INVALID; d need not be
  * a multiple of 8).  B, H >= 1, N >= 0; B * N < 2^31; H, H_kv < 2^16.  Pointers are aligned to the element size
  * (FA_ERR_ALIGN).  Pointers and strides that are multiples of 16 bytes, with rotary_dim and d multiples of two such
- * vectors, take the fast path (of 8 bytes in bf16: a little slower).
+ * vectors (rotary_dim of one when interleaved), take the fast path (of 8 bytes in bf16: a little slower).
  */
 typedef struct {
   int B, H, H_kv, N, d;
