@@ -7,7 +7,7 @@
 // carries the kernel is therefore bytes in flight and an even share for every SM:
 //
 //  * the keys of all (sequence, key/value head) pairs, in tiles of KT keys, are one
-//    line of work that is cut into equal ranges, one per warp (kPagedWorkers of them,
+//    line of work that is cut into equal ranges, one per warp (paged_workers of them,
 //    all resident at once), whatever the lengths are.  A range covers the end of one
 //    pair, whole pairs, and the beginning of another; whole pairs are written out,
 //    the cut ones leave (max, sum, O) partials that the merge kernel joins.  The
@@ -64,7 +64,7 @@ struct PagedArgs {
 
 // Keys of sequence b, 0 and flagged when the length makes no sense.
 __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
-  const int n = __ldg(a.seq_lens + b);
+  const int n = a.seq_lens[b];
   if (n < 0 || n > static_cast<long long>(a.max_pages) * a.page) {
     atomicOr(a.status, DEV_ARGS);
     return 0;
@@ -279,7 +279,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     if (8LL * mine < in.len) {
       const int e = mine / groups_per_page;
       row_next = (mine - e * groups_per_page) * 8;
-      pg_next = __ldg(a.table + in.b * a.table_stride + e);
+      pg_next = a.table[in.b * a.table_stride + e];
       if (pg_next < 0 || pg_next >= a.num_pages) {
         atomicOr(a.status, DEV_ARGS);
         pg_next = -1;

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(128) fa_pages_free_kernel(const PagesArgs a) {
   after_previous_kernel();
   const int i = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= a.n) return;
-  const int s = __ldg(a.seqs + i);
+  const int s = a.seqs[i];
   if (s < 0 || s >= a.S) {
     if (lane == 0) atomicOr(a.dev_status, DEV_ARGS);
     return;
@@ -368,9 +368,9 @@ __global__ void __launch_bounds__(256) fa_pages_copy_kernel(const PageCopyArgs a
     const long long mine = at + static_cast<long long>(lane) * teams;
     int my_src = -1, my_dst = 0, my_rows = 0;
     if (mine < a.n) {
-      my_src = __ldg(a.copies + 3 * mine);
-      my_dst = __ldg(a.copies + 3 * mine + 1);
-      my_rows = __ldg(a.copies + 3 * mine + 2);
+      my_src = a.copies[3 * mine];
+      my_dst = a.copies[3 * mine + 1];
+      my_rows = a.copies[3 * mine + 2];
     }
     unsigned todo = __ballot_sync(0xffffffffu, my_src >= 0);
     for (; todo; todo &= todo - 1) {

@@ -179,7 +179,8 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // A kernel that is launched while its predecessor in the stream still ends: everything the predecessor wrote is there
-// after this wait, and the next such kernel may come up.  Every thread, before it touches memory.
+// after this wait, and the next such kernel may come up.  Every thread, before it touches memory.  (What the predecessor
+// may have written is read with plain loads: the read-only path wants data that no one writes while the kernel exists.)
 __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

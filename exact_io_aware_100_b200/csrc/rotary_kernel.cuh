@@ -70,7 +70,7 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
   if constexpr (!APPEND) {
     k.b = static_cast<int>(t / a.N);
     k.row = static_cast<int>(t - static_cast<long long>(k.b) * a.N);
-    k.pos = a.pos ? __ldg(a.pos + k.b * a.pos_b + k.row) : k.row;
+    k.pos = a.pos ? a.pos[k.b * a.pos_b + k.row] : k.row;
     return k;
   } else {
     int back;                      // tokens of the sequence from this one to its last
@@ -79,9 +79,9 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
       int lo = 0, hi = a.B;        // the last b with cu[b] <= row
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu + mid) <= row) lo = mid; else hi = mid;
+        if (a.cu[mid] <= row) lo = mid; else hi = mid;
       }
-      const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1);
+      const int first = a.cu[lo], end = a.cu[lo + 1];
       k.b = lo;
       k.row = row;
       k.pos = 0;
@@ -93,7 +93,7 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
       k.row = static_cast<int>(t - static_cast<long long>(k.b) * a.N);
       back = a.N - k.row;
     }
-    const int len = __ldg(a.seq_lens + k.b);
+    const int len = a.seq_lens[k.b];
     k.pos = len - back;
     if (len < 0 || len > static_cast<long long>(a.max_pages) * a.page) {
       atomicOr(a.status, DEV_ARGS);
@@ -104,7 +104,7 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
     if (k.pos >= 0) {
       const int slot = k.pos / a.page;
       k.in_page = k.pos - slot * a.page;
-      k.page = __ldg(a.table + k.b * a.table_stride + slot);
+      k.page = a.table[k.b * a.table_stride + slot];
       if (k.page < 0 || k.page >= a.num_pages) {
         atomicOr(a.status, DEV_ARGS);
         k.skip = true;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a, int int
   const RotToken tk = rot_token<APPEND>(a, t);
   const bool turn = p < half;
   const int ca = turn ? (interleaved ? 2 * p : p) : p + half, cb = turn ? (interleaved ? 2 * p + 1 : p + half) : ca;
-  const float2 cs = turn ? rot_cos_sin(__ldg(a.freqs + p), tk.pos, a.magnitude, a.inverse) : make_float2(1.f, 0.f);
+  const float2 cs = turn ? rot_cos_sin(a.freqs[p], tk.pos, a.magnitude, a.inverse) : make_float2(1.f, 0.f);
   const bool pad = APPEND && (tk.skip || tk.page < 0);
   const int heads = pad ? (tk.skip && a.qo == a.q ? 0 : a.H) : a.H + (APPEND ? 2 : 1) * a.H_kv;
   const int h1 = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kRotThreads) fa_rotary_vec_kernel(const __grid
   for (int e = 0; e < V; ++e)
     if (e < V / 2 ? turn_a : turn_b) {
       const int pair = INTER ? (e < V / 2 ? ca : cb - V) / 2 + e : ca + e;
-      cs[e] = rot_cos_sin(__ldg(a.freqs + pair), tk.pos, a.magnitude, a.inverse);
+      cs[e] = rot_cos_sin(a.freqs[pair], tk.pos, a.magnitude, a.inverse);
     }
   asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1

@@ -304,3 +304,55 @@ def test_low_level_names_give_the_same():
 
     assert all(torch.equal(x, y) for x, y in zip(run(False), run(True)))
     _ok()
+
+
+def test_steps_in_a_row_give_what_single_steps_give():
+    """Every call may come up while the one before it ends: 60 steps with forks, ends and moves between them, queued
+    without a wait, against the same with a wait behind every call."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    S, P, M, page, H, H_kv, d = 40, 700, 24, 8, 8, 2, 64
+    freqs, _ = fa.rotary_frequencies(d)
+
+    def run(wait):
+        g = torch.Generator(device="cuda").manual_seed(5)
+        table = torch.full((S, M), -1, dtype=torch.int32, device="cuda")
+        lens, refs = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (S, P))
+        kp, vp = (torch.zeros(P, page, H_kv, d, device="cuda", dtype=torch.bfloat16).transpose(1, 2) for _ in range(2))
+        book, everyone = (table, lens, refs, page), _i(list(range(S)))
+        done = torch.cuda.synchronize if wait else (lambda: None)
+        outs = []
+        fa.pages_extend(*book, _i(list(range(20))), _i([3 * i + 1 for i in range(20)]))
+        grow = [_i([int(s < 20 + n) for s in range(S)]) for n in range(20)]
+        torch.cuda.synchronize()
+        for t in range(60):
+            q, k, v = (torch.randn(S, h, 1, d, device="cuda", generator=g).bfloat16() for h in (H, H_kv, H_kv))
+            done()
+            outs.append(fa.pages_extend(*book, everyone, grow[min(19, t // 2)]))
+            done()
+            q = fa.paged_append(k, v, kp, vp, table, lens, q=q, freqs=freqs)
+            done()
+            outs += fa.paged_decode(q, kp, vp, table, lens)
+            done()
+            if t % 2 == 0 and t // 2 < 18:
+                copies, status = fa.pages_fork(*book, _i([t // 2]), _i([20 + t // 2]))
+                done()
+                fa.pages_copy(kp, vp, copies)
+                outs += [copies, status]
+                done()
+            if t in (21, 45):
+                fa.pages_free(*book, _i([1, 30 + t % 7]))
+                done()
+                moves = fa.pages_compact(*book)
+                done()
+                fa.pages_copy(kp, vp, moves)
+                outs.append(moves)
+                done()
+        torch.cuda.synchronize()
+        return outs + [table, lens, refs, kp, vp]
+
+    want = run(True)
+    for _ in range(3):
+        got = run(False)
+        assert len(got) == len(want) and all(torch.equal(x, y) for x, y in zip(got, want))
+    _ok()
