@@ -12,8 +12,8 @@
 //    pair, whole pairs, and the beginning of another; whole pairs are written out,
 //    the cut ones leave (max, sum, O) partials that the merge kernel joins.  The
 //    lengths are read on the device: a captured call follows them.  When a table row
-//    holds a few tiles only, no pair is cut: there is nothing to plan and nothing to
-//    join, and the second launch falls away;
+//    holds a few tiles only, no pair is cut (paged_share): a warp or a block takes it,
+//    there is nothing to plan, and the second launch falls away;
 //  * a warp fills its own ring of tiles by TMA, across the ends of pairs, and waits for
 //    nobody: no block barrier in the loop.  Beginning and ending a pair (its rows'
 //    loads, its outputs) counts as kPagedPairUnits tiles.  A box is 8, 16 or 32 keys of
@@ -52,6 +52,7 @@ struct PagedArgs {
   int workers;                     // warps that share the work of one row tile
   int min_units;                   // least units of a warp's range
   int whole_units;                 // short tables: units of every pair, none of which is cut; else 0
+  int by_block;                    // short tables: a block to a pair, its tiles shared by the four warps; no partials
   int row_tiles;
   int part_rows;                   // rows of a partial
   float* part_o;                   // [row tile][worker][2][part_rows][D]
@@ -95,11 +96,27 @@ struct PagedCfg {
 };
 constexpr int kPagedSms = 148;
 constexpr int kPagedMinUnits = 2;                // of a range: what is in flight at once
-// Tiles of a table row up to which no pair is cut: 4, or 16 when there are pairs for half of the SMs' blocks.  One pair's
-// tiles one after the other take longer than in parts, but planning, partials and the second launch fall away.  Measured
-// uncut / cut: 16 x 8 pairs of 4 tiles (d 128) 6.7 / 10.4 us, of 8 tiles 10.0 / 10.6, of 12 tiles 13.1 / 11.0; 128 x 8 pairs
-// of 16 tiles 25.5 / 34.5; 128 x 4 pairs of 16 tiles (d 256) 35 / 44; 128 x 2 pairs of 16 tiles (24 rows) 31 / 23.
-__host__ __device__ inline int paged_whole_tiles(long long pairs) { return pairs >= 2 * 148 ? 16 : 4; }
+// How pairs whose table rows hold `tiles` tiles at most are shared out: each to a warp, each to a block's four warps, or
+// cut into ranges of equal length.  Uncut pairs take no planning, no partials and no second launch, but one warp's (or
+// four warps') time for their tiles.  Measured (device time, us; warp / block / cut; rows R per key/value head):
+//   8 pairs, d 128, R 4:     1 tile 3.9 / - / 7.0, 4 tiles 6.3 / - / 8.5, 8 tiles - / 4.8 / 9.1, 32 tiles - / 9.4 / 9.7,
+//                            64 tiles - / 15.8 / 10.6
+//   128 pairs:               8 tiles 10.0 / 5.1 / 10.6, 16 tiles 16.4 / 6.7 / 11.2, 64 tiles - / 16.5 / 17.4
+//   512 pairs:               8 tiles 9.7 / 11.2 / -, 16 tiles 16.3 / 14.8 / 21, 32 tiles - / 28 / 34
+//   1024 pairs:              16 tiles 25.5 / - / 34.5
+//   4 pairs, d 256, R 16:    8 tiles - / 11.4 / 13.3, 16 tiles - / 15.5 / 13.4;  64 pairs: 16 tiles - / 15.6 / 20.1;
+//                            256 pairs: 64 tiles - / 53 / 71
+enum PagedShare { kPagedCut, kPagedByWarp, kPagedByBlock };
+inline PagedShare paged_share(int d, int rm, long long pairs, long long tiles) {
+  const bool joins = rm <= 16;                     // blocks join their warps' parts up to 16 rows
+  if (pairs < 2 * 148) {
+    const int few = rm == 8 ? 32 : pairs < 32 ? (d == 256 ? 12 : 20) : d == 256 ? 24 : 32;
+    if (tiles <= (joins ? 1 : 4)) return kPagedByWarp;
+    return joins && tiles <= (pairs < 128 ? few : 64) ? kPagedByBlock : kPagedCut;
+  }
+  if (tiles <= (pairs < 4 * 148 && joins ? 12 : 16)) return kPagedByWarp;
+  return pairs < 4 * 148 && joins && tiles <= 64 ? kPagedByBlock : kPagedCut;
+}
 constexpr int kPagedTeam = 32;
 constexpr int kPagedPairUnits = 2;               // what beginning and ending a pair costs, in tiles
 
@@ -195,7 +212,17 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 
   long long t0, t1, range;
   PagedPlace in;                                   // the next tile to load
-  if (a.whole_units) {
+  if (a.by_block) {
+    // ---- this warp's quarter of the block's pair
+    __syncthreads();                               // abort_flag
+    in.b = blockIdx.x / a.H_kv;
+    in.h = blockIdx.x - in.b * a.H_kv;
+    in.enter<KT>(a);
+    in.tile = in.tiles * warp / C::WARPS;
+    in.unit = t0 = in.tile;
+    t1 = in.tiles * (warp + 1) / C::WARPS;         // t0 == t1: nothing for this warp
+    range = 1;
+  } else if (a.whole_units) {
     // ---- every pair has its place in the line, whatever its length
     const int pairs = a.B * a.H_kv, mine = (pairs + a.workers - 1) / a.workers;
     range = static_cast<long long>(mine) * a.whole_units;
@@ -258,13 +285,13 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
       in.unit = t0 + in.tile - u;
     }
   }
-  if (in.unit >= t1) return;
+  if (in.unit >= t1 && !a.by_block) return;
   // Do the block's four ranges lie inside one pair, and is it cut into kPagedTeam ranges at least?  (The same answer in all
   // four warps.)  Then they leave one partial: 33 MB of cache in 4 pairs (d 256) 23.7 -> 21 us with the merge.  With fewer
   // ranges the block's own joining costs more than it saves, and with 32 rows it takes registers that the loop needs.
   const long long tile0 = in.unit - in.tile, block0 = range * C::WARPS * blockIdx.x;
-  const bool team = RM <= 16 && !a.whole_units && block0 >= tile0 && block0 + range * C::WARPS <= tile0 + in.tiles &&
-                    in.tiles >= kPagedTeam * range;
+  const bool team = RM <= 16 && (a.by_block || (!a.whole_units && block0 >= tile0 && block0 + range * C::WARPS <= tile0 + in.tiles &&
+                                                in.tiles >= kPagedTeam * range));
   PagedPlace at = in;                              // the next tile to use
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
 
@@ -329,15 +356,14 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   uint32_t qf[MT][D / 16][C::HALF ? 2 : 4];
   float acc[MT][D / 8][4];
   float m[MT][RW], l[MT][RW];
-  // lane r holds where row r of the row tile lies behind its pair's first query head
-  const int my_row = rt * RM + lane, my_g = my_row / a.N, my_i = my_row - my_g * a.N;
-  const bool my_real = lane < RM && my_row < a.rows;
-  const long long q_row = my_real ? my_g * a.sq.h + my_i * a.sq.r : -1, o_row = my_g * a.so.h + my_i * a.so.r;
+  // lane r holds the query head (of the pair's) and position of row r of the row tile; head -1: there is none
+  const int my_row = rt * RM + lane, my_i = my_row % a.N, my_g = lane < RM && my_row < a.rows ? my_row / a.N : -1;
   // Q goes through the slot that is loaded next, a 16-row tile at a time, rows without a query as zeros.
   auto begin_pair = [&]() {
     const uint32_t to = ring + load_slot * C::SLOT;
     constexpr int CH = D / 8, RPI = 32 / CH, ROWS = C::HALF ? 8 : 16;   // 16-byte chunks of a row; rows per warp copy
     const int ch = lane % CH;
+    const long long q_row = my_g < 0 ? -1 : my_g * a.sq.h + my_i * a.sq.r;
     const __nv_bfloat16* q = a.q + at.b * a.sq.b + static_cast<long long>(at.h) * a.group * a.sq.h + ch * 8;
     const int row = (lane & 7) + (C::HALF ? 0 : ((lane >> 3) & 1) * 8), hi = C::HALF ? lane >> 3 : lane >> 4;
     const uint32_t qa = to + row * C::PITCH + ((hi ^ (row & 7)) << 4);
@@ -381,9 +407,10 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     __syncwarp();                                  // the slot is free for TMA
   };
   auto end_pair = [&](bool begins, bool ends) {    // of the pair's tiles this warp had the first, the last
-    const bool whole = begins && ends;
+    const bool whole = begins && ends && !a.by_block;
     const long long slot = ((static_cast<long long>(rt) * a.workers + worker) * 2 + (begins ? 1 : 0)) * a.part_rows;
     const long long head0 = static_cast<long long>(at.b) * a.H + at.h * a.group;
+    const long long o_row = my_g * a.so.h + my_i * a.so.r;
     __nv_bfloat16* o = a.o + at.b * a.so.b + static_cast<long long>(at.h) * a.group * a.so.h + 2 * quad;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -415,7 +442,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
           }
         }
       }
-    if (begins && !a.whole_units && lane == 0) {
+    if (begins && !a.whole_units && !a.by_block && lane == 0) {
       const int more = ends ? 0 : static_cast<int>((at.unit + at.tiles - 1 - at.tile) / range) - worker;
       a.meta[(static_cast<long long>(rt) * a.B + at.b) * a.H_kv + at.h] = make_int2(worker, more);
     }
@@ -433,9 +460,12 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   const int krow = (lane & 7) + ((lane >> 4) << 3), vrow = lane & 15;
   const uint32_t k_lane = key_at(krow) + ((((lane >> 3) & 1) ^ (krow & 7)) << 4);
   const uint32_t v_lane = key_at(vrow) + (((lane >> 4) ^ (vrow & 7)) << 4);
+  const bool busy = in.unit < t1;                  // (by_block: there may be nothing to do)
+  if (!busy)
+    for (int rr = lane; rr < RM; rr += 32) team_ml[warp * RM + rr] = make_float2(-INFINITY, 0.f);
   uint32_t p[MT][NT / 2][4];                       // per 16 keys: keys 0 .. 7 (rows, rows + 8), then keys 8 .. 15
 #pragma unroll 1
-  for (int ahead = C::SLOTS - 1;;) {               // tiles to load before the first is used
+  for (int ahead = C::SLOTS - 1; busy;) {          // tiles to load before the first is used
     if (ahead == 0) {
       if (fresh && !second) {                      // while the pair's first tile is on its way
         __syncwarp();                              // everyone is done with the free slot
@@ -592,8 +622,10 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     }
   }
   if (!team || !named_bar_and(1, C::THREADS, true)) return;
-  // ---- the block's four partials become one, in the slot of its first warp; the others' slots hold nothing
+  // ---- the block's four partials become one, in the slot of its first warp (the others' slots hold nothing), or, of a
+  // block's own pair, the output
   const int head = blockIdx.x * C::WARPS;
+  const long long o_row = my_g * a.so.h + my_i * a.so.r;
   for (int rr = warp; rr < min(RM, a.rows - rt * RM); rr += C::WARPS) {
     float2 ml[C::WARPS];
     float top = -INFINITY, sum = 0.f, w[C::WARPS];
@@ -604,24 +636,36 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     }
 #pragma unroll
     for (int x = 0; x < C::WARPS; ++x) {
-      w[x] = top == -INFINITY ? 1.f : exp2f(ml[x].x - top);
-      sum = fmaf(w[x], ml[x].y, sum);
+      w[x] = ml[x].x == -INFINITY ? 0.f : exp2f(ml[x].x - top);
+      sum += ml[x].x == -INFINITY ? ml[x].y : w[x] * ml[x].y;   // (0, or NaN from keys that are all NaN)
     }
     auto slot_of = [&](int x) {
       return ((static_cast<long long>(rt) * a.workers + head + x) * 2 + (x == 0 && block0 == tile0 ? 1 : 0)) * a.part_rows + rr;
     };
-    if (lane < C::WARPS) a.part_ml[slot_of(lane)] = lane == 0 ? make_float2(top, sum) : make_float2(-INFINITY, 0.f);
-    float* to = a.part_o + slot_of(0) * D;
+    const long long off = __shfl_sync(0xffffffffu, o_row, rr);
+    float f = 1.0f;
+    if (a.by_block) {
+      f = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+      if (lane == 0)
+        a.lse[(static_cast<long long>(at.b) * a.H + at.h * a.group) * a.N + rt * RM + rr] =
+            sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    } else if (lane < C::WARPS) {
+      a.part_ml[slot_of(lane)] = lane == 0 ? make_float2(top, sum) : make_float2(-INFINITY, 0.f);
+    }
+    float* part = a.part_o + slot_of(0) * D;
+    __nv_bfloat16* o = a.o + at.b * a.so.b + static_cast<long long>(at.h) * a.group * a.so.h + off;
 #pragma unroll
     for (int e = 2 * lane; e < D; e += 64) {
       float2 z = make_float2(0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < C::WARPS; ++x) {
         const float2 y = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(smem + x * C::RING) + rr * D + e);
+        if (ml[x].x == -INFINITY) continue;        // (a warp without tiles wrote nothing there)
         z.x = fmaf(w[x], y.x, z.x);
         z.y = fmaf(w[x], y.y, z.y);
       }
-      *reinterpret_cast<float2*>(to + e) = z;
+      if (a.by_block) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(z.x * f, z.y * f);
+      else *reinterpret_cast<float2*>(part + e) = z;
     }
   }
 }

@@ -110,9 +110,9 @@ fa_status check_decode(const fa_paged_layout& L) {
 
 // How a decode call is cut up, and where its workspace's parts lie.
 struct PagedPlan {
-  int rm, row_tiles, workers, part_rows, min_units, whole_units;
+  int rm, row_tiles, workers, part_rows, min_units, whole_units, by_block;
   size_t o_bytes, ml_bytes, meta_bytes;            // none is needed when no pair is cut
-  size_t bytes() const { return whole_units ? 256 : o_bytes + ml_bytes + meta_bytes; }
+  size_t bytes() const { return whole_units || by_block ? 256 : o_bytes + ml_bytes + meta_bytes; }
 };
 PagedPlan paged_plan(const fa_paged_layout& L) {
   PagedPlan p;
@@ -125,11 +125,14 @@ PagedPlan paged_plan(const fa_paged_layout& L) {
   p.min_units = std::max(kPagedMinUnits, 2 * p.part_rows / kt);
   // no more warps than the longest sequences that the table can hold give work to
   const long long most = (1LL * L.max_pages * L.page_size + kt - 1) / kt, pairs = 1LL * L.B * L.H_kv;
-  p.whole_units = most <= paged_whole_tiles(pairs) ? static_cast<int>(most) + kPagedPairUnits : 0;
+  const PagedShare share = paged_share(L.d, p.rm, pairs, most);
+  p.whole_units = share == kPagedByWarp ? static_cast<int>(most) + kPagedPairUnits : 0;
+  p.by_block = share == kPagedByBlock;
   const long long units = p.whole_units ? pairs : (most + kPagedPairUnits) * pairs, least = p.whole_units ? 1 : p.min_units;
   const long long ctas = (units + 4 * least - 1) / (4 * least);
   p.workers = paged_workers(p.row_tiles);
   if (ctas < p.workers / 4) p.workers = static_cast<int>(ctas) * 4;
+  if (p.by_block) p.workers = static_cast<int>(pairs) * 4;
   const size_t parts = 2 * static_cast<size_t>(p.row_tiles) * p.workers * p.part_rows;
   p.o_bytes = round256(parts * L.d * 4);
   p.ml_bytes = round256(parts * 8);
@@ -166,7 +169,7 @@ fa_status launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Paged
   }
   const fa_status st = launch(fa_paged_decode_kernel<D, RM>, dim3(a.workers / C::WARPS, a.row_tiles), C::THREADS, C::SMEM, s,
                               tk, tv, a);
-  if (st != FA_OK || a.whole_units) return st;
+  if (st != FA_OK || a.whole_units || a.by_block) return st;
   // the merge: 8, 4, 2 or 1 warps to a row, as many as the GPU holds at once
   const long long rows = 1LL * a.B * a.H * a.N;
   const int per_row = rows <= kPagedSms * 8 ? 8 : rows <= kPagedSms * 16 ? 4 : rows <= kPagedSms * 32 ? 2 : 1;
@@ -379,6 +382,7 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   a.part_rows = plan.part_rows;
   a.min_units = plan.min_units;
   a.whole_units = plan.whole_units;
+  a.by_block = plan.by_block;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + plan.o_bytes);

@@ -342,17 +342,12 @@ def _reference(q, kp, vp, table, lens, causal, scale):
     return o, lse
 
 
-@pytest.mark.parametrize("seed", range(40))
-def test_decode_anywhere_in_the_range(seed):
-    """Sizes, lengths and layouts at random: cut and uncut pairs, every row tile, every box, idle and tiny sequences."""
+def _random_decode(seed, rng, d, page, H_kv, group, N, B, most, idle):
+    """One call on random lengths up to `most`, NaN wherever no key is, against float64."""
     import torch
     import exact_io_aware_100_b200 as fa
-    rng = np.random.default_rng(9000 + seed)
     pick = lambda *x: x[int(rng.integers(len(x)))]  # noqa: E731
-    d, page, H_kv, group, N = pick(64, 128, 256), pick(8, 16, 24, 32, 48, 64, 128), pick(1, 2, 5, 8), pick(1, 2, 3, 4, 8), pick(1, 1, 2, 4, 9)
-    B = int(np.exp(rng.uniform(0, np.log(160))))
-    most = int(np.exp(rng.uniform(0, np.log(min(20000, 6_000_000 // (B * H_kv * d) * 8 + 2)))))
-    lens = [most] + [int(np.exp(rng.uniform(0, np.log(most + 0.99)))) - pick(0, 0, 1) for _ in range(B - 1)]
+    lens = [most] + [int(np.exp(rng.uniform(0, np.log(most + 0.99)))) - pick(0, 0, idle) for _ in range(B - 1)]
     P = sum(-(-n // page) for n in lens) + 3
     kp, vp = _cache(P, H_kv, page, d, pick(True, False), fill=NAN)
     table, sl = _table(lens, page, P, M=-(-most // page) + pick(0, 0, 7), seed=seed)
@@ -375,6 +370,30 @@ def test_decode_anywhere_in_the_range(seed):
     assert np.array_equal(np.isneginf(got), empty) and not np.isnan(got).any()
     assert (np.abs(got[~empty] - rl[~empty]) <= 1e-5 * np.maximum(1, np.abs(rl[~empty]))).all()
     assert not to_f64(o)[empty].any()
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_decode_anywhere_in_the_range(seed):
+    """Sizes, lengths and layouts at random: cut and uncut pairs, every row tile, every box, idle and tiny sequences."""
+    rng = np.random.default_rng(9000 + seed)
+    pick = lambda *x: x[int(rng.integers(len(x)))]  # noqa: E731
+    d, page, H_kv, group, N = pick(64, 128, 256), pick(8, 16, 24, 32, 48, 64, 128), pick(1, 2, 5, 8), pick(1, 2, 3, 4, 8), pick(1, 1, 2, 4, 9)
+    B = int(np.exp(rng.uniform(0, np.log(160))))
+    most = int(np.exp(rng.uniform(0, np.log(min(20000, 6_000_000 // (B * H_kv * d) * 8 + 2)))))
+    _random_decode(seed, rng, d, page, H_kv, group, N, B, most, 1)
+
+
+@pytest.mark.parametrize("seed", range(36))
+def test_decode_short_tables(seed):
+    """Tables of 1 to 70 tiles and 1 to 1300 pairs: pairs of a warp, of a block, and cut ones, one query row to 40."""
+    rng = np.random.default_rng(400 + seed)
+    pick = lambda *x: x[int(rng.integers(len(x)))]  # noqa: E731
+    d = (64, 128, 256)[seed % 3]
+    H_kv = pick(1, 2, 4, 8)
+    B = max(1, int(np.exp(rng.uniform(0, np.log(1300 / H_kv)))))
+    tiles = int(np.exp(rng.uniform(0, np.log(70))))
+    most = max(1, tiles * (32 if d == 64 else 16) - pick(0, 1, 5, 15))
+    _random_decode(seed, rng, d, pick(8, 16, 40, 64), H_kv, pick(1, 2, 4, 8), pick(1, 1, 1, 2, 5), B, most, 1)
 
 
 def test_calls_from_several_threads():
