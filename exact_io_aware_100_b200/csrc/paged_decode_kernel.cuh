@@ -120,8 +120,14 @@ inline PagedShare paged_share(int d, int rm, long long pairs, long long tiles) {
 constexpr int kPagedTeam = 32;
 constexpr int kPagedPairUnits = 2;               // what beginning and ending a pair costs, in tiles
 
-// Rows of a row tile: rounded up to 8, 16 or (d < 256) 32.
-__host__ __device__ inline int paged_row_tile(int d, int rows) { return rows <= 8 ? 8 : rows <= 16 || d == 256 ? 16 : 32; }
+// Rows of a row tile: 8, 16 or (d < 256, long calls) 32.  Two tiles of 16 read every key twice, once of that from L2, but
+// take half the time per tile; `tiles` are those of all pairs.  16 / 32, us: 32 rows, d 128, 64 pairs of 64 tiles 21 / 24, of
+// 256 tiles 42 / 52, of 1024 tiles 130 / 121; 24 rows, d 64, 2 pairs of 8 tiles 6.3 / 10.3, 32 pairs of 32 tiles 12.4 / 14.0,
+// of 128 tiles 19.4 / 17.7, 256 pairs of 512 tiles 269 / 200.
+inline int paged_row_tile(int d, int rows, long long tiles) {
+  if (rows <= 8) return 8;
+  return rows <= 16 || d == 256 || tiles <= (d == 64 ? 2 : 14) * 1184LL ? 16 : 32;
+}
 // Warps that share one row tile's work.
 __host__ __device__ inline int paged_workers(int row_tiles) {
   const int ctas = kPagedSms * 2 / row_tiles;

@@ -116,16 +116,16 @@ struct PagedPlan {
 };
 PagedPlan paged_plan(const fa_paged_layout& L) {
   PagedPlan p;
-  const int rows = L.H / L.H_kv * L.N;
-  p.rm = paged_row_tile(L.d, rows);
+  const int rows = L.H / L.H_kv * L.N, kt = L.d == 64 ? 32 : 16;
+  // the longest sequences that the table can hold, in tiles
+  const long long most = (1LL * L.max_pages * L.page_size + kt - 1) / kt, pairs = 1LL * L.B * L.H_kv;
+  p.rm = paged_row_tile(L.d, rows, most * pairs);
   p.row_tiles = (rows + p.rm - 1) / p.rm;
   p.part_rows = rows < p.rm ? rows : p.rm;
   // A range's partial (4 d bytes a row) should be no more than half of its keys (4 d bytes each)
-  const int kt = L.d == 64 ? 32 : 16;
   p.min_units = std::max(kPagedMinUnits, 2 * p.part_rows / kt);
-  // no more warps than the longest sequences that the table can hold give work to
-  const long long most = (1LL * L.max_pages * L.page_size + kt - 1) / kt, pairs = 1LL * L.B * L.H_kv;
-  const PagedShare share = paged_share(L.d, p.rm, pairs, most);
+  // no more warps than those sequences give work to
+  const PagedShare share = paged_share(L.d, p.rm, pairs * p.row_tiles, most);
   p.whole_units = share == kPagedByWarp ? static_cast<int>(most) + kPagedPairUnits : 0;
   p.by_block = share == kPagedByBlock;
   const long long units = p.whole_units ? pairs : (most + kPagedPairUnits) * pairs, least = p.whole_units ? 1 : p.min_units;
