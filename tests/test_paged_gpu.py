@@ -429,3 +429,56 @@ def test_calls_from_several_threads():
     for t in threads:
         t.join()
     assert not bad and fa.fa_get_device_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("d,page,H_kv,group,N,B,most", [
+    (64, 8, 1, 4, 1, 3000, 700),       # more sequences than planning threads, most of them short, some empty
+    (128, 16, 2, 2, 300, 1, 1000),     # a piece of a prompt: 600 rows per key/value head
+    (64, 32, 1, 2, 70, 3, 40),         # more queries than keys
+    (256, 64, 2, 3, 40, 2, 5000),
+    (128, 24, 1, 1, 1, 1, 30000),      # one pair over the whole GPU
+])
+def test_decode_large_in_one_way(d, page, H_kv, group, N, B, most):
+    _random_decode(77, np.random.default_rng(d + N), d, page, H_kv, group, N, B, most, 1)
+
+
+def test_decode_bad_pages_in_a_long_table_are_reported():
+    """As above, where pairs are cut: other sequences keep their results."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    lens, page = [2000, 2000, 2000], 16
+    P = 400
+    kp, vp = _cache(P, 2, page, 64, True)
+    table, sl = _table(lens, page, P, M=300)
+    _fill(kp, vp, table, lens, page)
+    q = torch.randn(3, 4, 1, 64, device="cuda").bfloat16()
+    good, glse = fa.paged_decode(q, kp, vp, table, sl)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    for bad_page, bad_len in ((P, 2000), (-1, 2000), (2**31 - 1, 2000), (5, -3), (5, 4801), (5, 2**31 - 1)):
+        t, n = table.clone(), sl.clone()
+        t[1, 100], n[1] = bad_page, bad_len
+        o, lse = fa.paged_decode(q, kp, vp, t, n)
+        assert fa.fa_get_device_status() == fa.FA_ERR_INVALID
+        if bad_len == 2000:                          # the line is cut at the same places: the same bits
+            assert torch.equal(o[0], good[0]) and torch.equal(o[2], good[2])
+        # else: other partial sums, each of them 32-bit, and one rounding of o
+        assert ((o[[0, 2]].float() - good[[0, 2]].float()).abs() <= 2.0 ** -7 * good[[0, 2]].float().abs() + 1e-6).all()
+        assert (lse[[0, 2]] - glse[[0, 2]]).abs().max() < 1e-5
+
+
+def test_keys_and_values_that_are_not_finite():
+    """A NaN or an infinity among the keys a row sees comes out as NaN, in the rows that see it only."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    for n, M in ((60, 4), (3000, 188)):
+        kp, vp = _cache(400, 2, 16, 64, True)
+        table, sl = _table([n, n], 16, 400, M=M)
+        q = torch.randn(2, 4, 1, 64, device="cuda").bfloat16()
+        for pages, value in ((kp, NAN), (vp, NAN), (vp, float("inf"))):
+            _fill(kp, vp, table, [n, n], 16)
+            want = fa.paged_decode(q, kp, vp, table, sl)
+            pages[int(table[0, 1]), 1, 3] = value    # head 1 of sequence 0
+            o, lse = fa.paged_decode(q, kp, vp, table, sl)
+            assert torch.equal(o[1], want[0][1]) and torch.equal(o[0, :2], want[0][0, :2])
+            assert not torch.isfinite(o[0, 2:].float()).any()
+            assert torch.isnan(lse[0, 2:]).all() if pages is kp else torch.equal(lse, want[1])
