@@ -110,7 +110,7 @@ enum PagedShare { kPagedCut, kPagedByWarp, kPagedByBlock };
 inline PagedShare paged_share(int d, int rm, long long pairs, long long tiles) {
   const bool joins = rm <= 16;                     // blocks join their warps' parts up to 16 rows
   if (pairs < 2 * 148) {
-    const int few = rm == 8 ? 32 : pairs < 32 ? (d == 256 ? 12 : 20) : d == 256 ? 24 : 32;
+    const int few = pairs >= 32 ? (rm == 16 && d == 256 ? 24 : 32) : d == 256 ? (rm == 8 ? 20 : 12) : rm == 8 ? 32 : 20;
     if (tiles <= (joins ? 1 : 4)) return kPagedByWarp;
     return joins && tiles <= (pairs < 128 ? few : 64) ? kPagedByBlock : kPagedCut;
   }
@@ -120,12 +120,16 @@ inline PagedShare paged_share(int d, int rm, long long pairs, long long tiles) {
 constexpr int kPagedTeam = 32;
 constexpr int kPagedPairUnits = 2;               // what beginning and ending a pair costs, in tiles
 
-// Rows of a row tile: 8, 16 or (d < 256, long calls) 32.  Two tiles of 16 read every key twice, once of that from L2, but
-// take half the time per tile; `tiles` are those of all pairs.  16 / 32, us: 32 rows, d 128, 64 pairs of 64 tiles 21 / 24, of
-// 256 tiles 42 / 52, of 1024 tiles 130 / 121; 24 rows, d 64, 2 pairs of 8 tiles 6.3 / 10.3, 32 pairs of 32 tiles 12.4 / 14.0,
-// of 128 tiles 19.4 / 17.7, 256 pairs of 512 tiles 269 / 200.
-inline int paged_row_tile(int d, int rows, long long tiles) {
-  if (rows <= 8) return 8;
+// Rows of a row tile: 8, 16 or (d < 256) 32.  Small row tiles read every key several times, but once only from HBM, and take
+// a warp less time per tile: what counts while calls are short and blocks fit the GPU at once.  `tiles` are those of all
+// pairs.  Device time, us, by the rows of a tile:
+//   16 rows, d 256, 4 pairs of 8 tiles (8 / 16) 7.4 / 10.8, of 256 tiles 16.5 / 18.2; 64 pairs of 64 tiles 25.5 / 25.7
+//   16 rows, d 128, 64 pairs of 8 tiles 5.7 / 7.3, of 32 tiles 10.6 / 12.3, of 256 tiles 39.7 / 36.6; 256 pairs of 8 10.0 / 8.1
+//   32 rows, d 128, 64 pairs of 64 tiles (16 / 32) 21 / 24, of 256 tiles 42 / 52, of 1024 tiles 130 / 121
+//   24 rows, d 64, 2 pairs of 8 tiles 6.3 / 10.3, 32 pairs of 32 tiles 12.4 / 14.0, of 128 tiles 19.4 / 17.7
+inline int paged_row_tile(int d, int rows, long long pairs, long long tiles) {
+  const int eights = (rows + 7) / 8;
+  if (eights == 1 || (eights <= 4 && pairs * eights < 2 * 148 && tiles <= (d == 256 ? 4 : 2) * 1184LL)) return 8;
   return rows <= 16 || d == 256 || tiles <= (d == 64 ? 2 : 14) * 1184LL ? 16 : 32;
 }
 // Warps that share one row tile's work.

@@ -119,7 +119,7 @@ PagedPlan paged_plan(const fa_paged_layout& L) {
   const int rows = L.H / L.H_kv * L.N, kt = L.d == 64 ? 32 : 16;
   // the longest sequences that the table can hold, in tiles
   const long long most = (1LL * L.max_pages * L.page_size + kt - 1) / kt, pairs = 1LL * L.B * L.H_kv;
-  p.rm = paged_row_tile(L.d, rows, most * pairs);
+  p.rm = paged_row_tile(L.d, rows, pairs, most * pairs);
   p.row_tiles = (rows + p.rm - 1) / p.rm;
   p.part_rows = rows < p.rm ? rows : p.rm;
   // A range's partial (4 d bytes a row) should be no more than half of its keys (4 d bytes each)

@@ -330,7 +330,8 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
  * the pages hold behind a sequence's end does not matter (NaN included); a key
  * that only some of the N queries see has to be finite.  Scores, softmax and sums
  * are 32-bit; the probabilities enter the second product with 16 bits of mantissa
- * when H / H_kv * N <= 8, else rounded to bf16; o is rounded once.
+ * when H / H_kv * N <= 8 (and in some short calls with more), else rounded to bf16;
+ * o is rounded once.
  * workspace: at least fa_paged_decode_workspace_size(layout) bytes, 256-byte
  * aligned; not shared by calls that may overlap.
  */
