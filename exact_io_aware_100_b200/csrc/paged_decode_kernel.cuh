@@ -37,13 +37,13 @@
 namespace fa {
 
 struct PagedArgs {
-  const __nv_bfloat16 *q, *kp, *vp;
+  const __nv_bfloat16* q;          // (the pages come through the tensor maps)
   __nv_bfloat16* o;
   float* lse;                      // [B, H, N]
   const int* table;
   long long table_stride;
   const int* seq_lens;
-  Strides sq, so, skp, svp;        // skp, svp: {page, head, row}
+  Strides sq, so;
   int B, H, H_kv, N, group;
   int rows;                        // group * N
   int num_pages, page, max_pages;
@@ -166,8 +166,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // A place in the line: tile `tile` of the `tiles` of (sequence b, key/value head h), which is `unit` of the line.
 struct PagedPlace {
@@ -386,7 +385,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         copy16(to + rr * C::PITCH + ((ch ^ (rr & 7)) << 4), off < 0 ? a.q : q + off, off >= 0);
       }
       copy_commit();
-      copy_wait<0>();
+      copy_wait_all();
       __syncwarp();
       if constexpr (C::HALF) {                     // two k-steps at a time: chunks 4 x .. 4 x + 3
 #pragma unroll

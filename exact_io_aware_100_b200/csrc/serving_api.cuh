@@ -354,8 +354,6 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   if ((st = device_state(&ds)) != FA_OK) return st;
   PagedArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(q);
-  a.kp = static_cast<const __nv_bfloat16*>(k_pages);
-  a.vp = static_cast<const __nv_bfloat16*>(v_pages);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   a.table = page_table;
@@ -363,8 +361,6 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
   a.seq_lens = seq_lens;
   a.sq = kstrides(L.q);
   a.so = kstrides(L.o);
-  a.skp = kstrides(L.k_pages);
-  a.svp = kstrides(L.v_pages);
   a.B = L.B;
   a.H = L.H;
   a.H_kv = L.H_kv;
