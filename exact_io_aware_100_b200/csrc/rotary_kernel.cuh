@@ -33,6 +33,8 @@ struct RotArgs {
   long long table_stride;
   const int* seq_lens;
   const int* cu;                   // packed offsets, or null
+  const int* new_tokens;           // tokens among a sequence's rows (its last ones), or null: all
+  const int* refused;              // not 0: none of the sequence's rows is a token; or null
   int total;
   int num_pages, page, max_pages;
   uint32_t* status;
@@ -73,7 +75,7 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
     k.pos = a.pos ? a.pos[k.b * a.pos_b + k.row] : k.row;
     return k;
   } else {
-    int back;                      // tokens of the sequence from this one to its last
+    int back, rows;                // rows of the sequence from this one to its last; all of them
     if (a.cu) {
       const int row = static_cast<int>(t);
       int lo = 0, hi = a.B;        // the last b with cu[b] <= row
@@ -86,22 +88,34 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
       k.row = row;
       k.pos = 0;
       back = end - row;
+      rows = end - first;
       if (row < first || row >= end) { k.skip = true; return k; }
       if (first < 0 || end > a.total) { atomicOr(a.status, DEV_ARGS); k.skip = true; return k; }
     } else {
       k.b = static_cast<int>(t / a.N);
       k.row = static_cast<int>(t - static_cast<long long>(k.b) * a.N);
-      back = a.N - k.row;
+      rows = a.N;
+      back = rows - k.row;
     }
-    const int len = a.seq_lens[k.b];
+    // (independent loads: none waits for another)
+    const int len = a.seq_lens[k.b], fresh = a.new_tokens ? a.new_tokens[k.b] : rows, no = a.refused ? a.refused[k.b] : 0;
     k.pos = len - back;
+    if (no != 0) {
+      k.page = -1;
+      return k;
+    }
+    if (fresh < 0 || fresh > rows) {
+      atomicOr(a.status, DEV_ARGS);
+      k.skip = true;
+      return k;
+    }
     if (len < 0 || len > static_cast<long long>(a.max_pages) * a.page) {
       atomicOr(a.status, DEV_ARGS);
       k.skip = true;
       return k;
     }
     k.page = -1;
-    if (k.pos >= 0) {
+    if (k.pos >= 0 && back <= fresh) {
       const int slot = k.pos / a.page;
       k.in_page = k.pos - slot * a.page;
       k.page = a.table[k.b * a.table_stride + slot];

@@ -291,7 +291,8 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
   if (tokens == 0) return FA_OK;
   const int nb = pk ? 1 : L.B, rows = pk ? L.total : L.N;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned_to(page_table, 4) ||
-      !aligned_to(seq_lens, 4) || (pk && !aligned_to(L.cu_seqlens, 4)) || (freqs != nullptr && !aligned_to(freqs, 8)) ||
+      !aligned_to(seq_lens, 4) || (pk && !aligned_to(L.cu_seqlens, 4)) || (L.tokens != nullptr && !aligned_to(L.tokens, 4)) ||
+      (L.status != nullptr && !aligned_to(L.status, 4)) || (freqs != nullptr && !aligned_to(freqs, 8)) ||
       (q != nullptr && (!aligned16(q) || !aligned16(o))) || !strides_ok(L.k, rows, L.H_kv, nb) ||
       !strides_ok(L.v, rows, L.H_kv, nb) ||
       (q != nullptr && (!strides_ok(L.q, rows, L.H, nb) || !strides_ok(L.o, rows, L.H, nb))))
@@ -324,6 +325,8 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
   a.table_stride = L.table_stride;
   a.seq_lens = seq_lens;
   a.cu = L.cu_seqlens;
+  a.new_tokens = L.tokens;
+  a.refused = L.status;
   a.total = L.total;
   a.num_pages = L.num_pages;
   a.page = L.page_size;

@@ -255,15 +255,16 @@ void table(const Tensor& page_table, const Tensor& seq_lens, int64_t batch, fa_p
   L->table_stride = page_table.stride(0);
 }
 
-// paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, interleaved, magnitude, cu_seqlens, out)
+// paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, interleaved, magnitude, cu_seqlens, out, tokens, status)
 PyObject* paged_append(PyObject* const* args, Py_ssize_t n) {
-  arguments(n, 12);
+  arguments(n, 14);
   const Tensor &k = tensor(args[0], "k"), &v = tensor(args[1], "v");
   const Tensor &kp = tensor(args[2], "k_pages"), &vp = tensor(args[3], "v_pages");
   const Tensor &pt = tensor(args[4], "page_table"), &lens = tensor(args[5], "seq_lens");
   const Tensor *q = optional_tensor(args[6], "q"), *freqs = optional_tensor(args[7], "freqs");
   const double magnitude = number(args[9]);
   const Tensor *cu = optional_tensor(args[10], "cu_seqlens"), *out = optional_tensor(args[11], "out");
+  const Tensor *counts = optional_tensor(args[12], "tokens"), *status = optional_tensor(args[13], "status");
   const bool packed = cu != nullptr;
   fa_paged_layout L = {};
   cache(kp, vp, &L);
@@ -277,6 +278,11 @@ PyObject* paged_append(PyObject* const* args, Py_ssize_t n) {
     TORCH_CHECK_VALUE(cu->size(0) >= 1, "cu_seqlens: expected B + 1 offsets");
   }
   table(pt, lens, packed ? cu->size(0) - 1 : k.size(0), &L);
+  for (const Tensor* t : {counts, status}) {
+    if (t == nullptr) continue;
+    int32_tensor(*t, t == counts ? "tokens" : "status", 1);
+    TORCH_CHECK_VALUE(t->size(0) == L.B, t == counts ? "tokens" : "status", ": expected one per sequence of the batch");
+  }
   L.N = packed ? 0 : extent(k.size(2));
   L.total = packed ? extent(k.size(0)) : 0;
   if (q != nullptr) {
@@ -293,7 +299,7 @@ PyObject* paged_append(PyObject* const* args, Py_ssize_t n) {
   std::optional<Tensor> o;
   {
     Unlocked u;
-    Place place({&k, &v, &kp, &vp, &pt, &lens, q, freqs, cu, out});
+    Place place({&k, &v, &kp, &vp, &pt, &lens, q, freqs, cu, out, counts, status});
     if (out != nullptr) o = *out;
     else if (q != nullptr) o = at::empty_like(*q);
     L.q = strides(q);
@@ -301,6 +307,8 @@ PyObject* paged_append(PyObject* const* args, Py_ssize_t n) {
     L.k = strides(&k);
     L.v = strides(&v);
     L.cu_seqlens = data<int32_t>(cu);
+    L.tokens = data<int32_t>(counts);
+    L.status = data<int32_t>(status);
     check(lib.paged_append(data<void>(q), data<void>(k), data<void>(v), o ? data<void>(*o) : nullptr, data<void>(kp),
                            data<void>(vp), data<int32_t>(pt), data<int32_t>(lens), data<double>(freqs), &L,
                            static_cast<float>(magnitude), place.stream),

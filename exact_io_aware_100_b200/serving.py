@@ -8,9 +8,14 @@ generation step makes several of these calls and their kernels take a few micros
 
 A serving step of a batch of sequences, all of it on the device and capturable into a CUDA graph:
 
-    pages_extend(page_table, seq_lens, refcounts, page_size, seqs, tokens)      # lengths grow, pages are found
-    q = paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q=q, freqs=freqs)
+    status = pages_extend(page_table, seq_lens, refcounts, page_size, seqs, tokens)    # lengths grow, pages are found
+    q = paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q=q, freqs=freqs, tokens=tokens, status=status)
     o, lse = paged_decode(q, k_pages, v_pages, page_table, seq_lens)
+
+``seqs`` are the batch's sequences in their order (the rows of ``page_table``), ``tokens`` what each of them gets in this
+step.  Append takes both ``tokens`` and ``status``, so that a sequence that is idle (0 tokens) or whose request was refused
+(no page left) keeps its cache as it was; its rows of q are zero, and its rows of o mean nothing.  After the step the host
+reads ``status``, makes room for the refused (frees or moves sequences) and gives them the same token again.
 
 Tensors may live on any CUDA device; a call runs on their device, on that device's current stream or on
 ``stream``.  With ``stream`` the outputs are allocated on it and the inputs are recorded as in use there.
@@ -40,7 +45,8 @@ class FaPagedLayout(ctypes.Structure):
     """fa_paged_layout (include/fa.h), its strides flat."""
     _fields_ = [(n, _I32) for n in ("B", "H", "H_kv", "d", "N", "num_pages", "page_size", "max_pages")] + \
                [("table_stride", _I64)] + _axes("q", "o", "k", "v", "k_pages", "v_pages") + \
-               [("cu_seqlens", _VP), ("total", _I32), ("rotary_dim", _I32), ("interleaved", _I32)]
+               [("cu_seqlens", _VP), ("total", _I32), ("rotary_dim", _I32), ("interleaved", _I32), ("tokens", _VP),
+                ("status", _VP)]
 
 
 class FaPagesLayout(ctypes.Structure):
@@ -255,7 +261,7 @@ def rotary_backward(dq, dk, freqs, positions=None, interleaved: bool = False, ma
 
 # ----------------------------------------------------------------- the paged cache
 def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q=None, freqs=None, interleaved: bool = False,
-                 magnitude: float = 1.0, cu_seqlens=None, out=None, stream=None):
+                 magnitude: float = 1.0, cu_seqlens=None, out=None, stream=None, tokens=None, status=None):
     """Writes new keys and values (bf16) into the cache k_pages, v_pages [pages, H_kv, page_size, d] (any strides; pages of
     [pages, page_size, H_kv, d] memory are passed as their transpose(1, 2)), and returns q turned (None without q).
 
@@ -263,13 +269,17 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q=None, freqs=Non
     lengths after the call: token i of the n of sequence b goes to position seq_lens[b] - n + i.  With ``freqs`` the
     keys, and q [B, H, N, d] (or packed), are turned as by ``rotary`` at those positions.  A token whose position would
     be negative is padding: not written, and zero in the returned q; so are packed rows outside every sequence, which keep
-    their values when ``out`` is q itself."""
+    their values when ``out`` is q itself.
+
+    ``tokens`` (int32 [B]): only the last tokens[b] of sequence b's rows are tokens, the others padding.  ``status`` (int32
+    [B], as ``pages_extend`` returns it): a sequence whose entry is not FA_OK has none.  Without them every sequence has n new
+    tokens, and one that did not grow by n before the call loses its last cached keys and values to them."""
     if stream is not None:
-        with _On(stream, k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, cu_seqlens, out):
+        with _On(stream, k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, cu_seqlens, out, tokens, status):
             return paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, interleaved, magnitude, cu_seqlens,
-                                out)
+                                out, None, tokens, status)
     return (_ext or _native()).paged_append(k, v, k_pages, v_pages, page_table, seq_lens, q, freqs, interleaved, magnitude,
-                                            cu_seqlens, out)
+                                            cu_seqlens, out, tokens, status)
 
 
 def paged_decode(q, k_pages, v_pages, page_table, seq_lens, causal: bool = True, scale: float | None = None, stream=None,
@@ -287,7 +297,7 @@ def pages_extend(page_table, seq_lens, refcounts, page_size: int, seqs, tokens, 
     """Sequences ``seqs`` (int32 [n]) grow by ``tokens`` (int32 [n]) positions and get the pages they need: the free ones
     of lowest number, in the order of the requests.  page_table [S, max_pages], seq_lens [S] and refcounts [pages] (int32)
     are updated in place.  Returns status int32 [n]: FA_OK, FA_ERR_WORKSPACE (no page left) or FA_ERR_INVALID; a request
-    that is not FA_OK changed nothing."""
+    that is not FA_OK changed nothing (and ``paged_append`` with this status and the same tokens writes nothing for it)."""
     if stream is not None:
         with _On(stream, page_table, seq_lens, refcounts, seqs, tokens, workspace):
             return pages_extend(page_table, seq_lens, refcounts, page_size, seqs, tokens, None, workspace)

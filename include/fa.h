@@ -300,6 +300,8 @@ typedef struct {
   const int32_t* cu_seqlens;    /* fa_paged_append, packed: DEVICE B + 1 row offsets; else NULL */
   int total;                    /* packed: rows of q, k, v                                      */
   int rotary_dim, interleaved;  /* fa_paged_append with freqs                                   */
+  const int32_t* tokens;        /* fa_paged_append: DEVICE [B], new tokens of each sequence; NULL: all of its rows */
+  const int32_t* status;        /* fa_paged_append: DEVICE [B], not 0: the sequence has no new tokens; or NULL     */
 } fa_paged_layout;
 
 /*
@@ -312,6 +314,15 @@ typedef struct {
  * positions.  q != NULL: the queries ([.][H][.][d]) are turned the same way into
  * o, which may be q (same strides).  A token whose position is negative (a
  * sequence shorter than n: padding) is not written and its row of o is zero.
+ * layout->tokens: only the last tokens[b] of sequence b's n rows are tokens,
+ * the rows before them padding; a count outside 0 .. n is reported by
+ * fa_get_device_status as FA_ERR_INVALID and nothing of that sequence is
+ * written.  layout->status: rows of a sequence whose entry is not FA_OK are
+ * padding, whatever its count.  With the tokens given to fa_pages_extend and
+ * the status it returned (for the batch's sequences in their order), idle and
+ * refused sequences, whose lengths did not grow, keep their cache as it was.
+ * Without them every sequence gets n tokens: one that did not grow by n has
+ * its last cached rows overwritten, on pages that others may share.
  * A packed row outside every sequence is not written either; its row of o is
  * zero, or what it was when o is q.  Two sequences must not receive tokens
  * on the same page.  H is only used with q; H, H_kv < 2^16.
@@ -364,7 +375,8 @@ size_t fa_paged_decode_workspace_size(const fa_paged_layout* layout);
  *   the last; page_table and refcounts name the new places.
  * status[i] (extend, fork): 0 done; FA_ERR_WORKSPACE: no page left (a request is granted when the pages that it and all
  *   valid requests before it need were free); FA_ERR_INVALID: a sequence number out of range or asked for twice in one call, a
- *   negative length or count, more than max_pages pages, dst not empty.  A request that is not granted changes nothing.
+ *   negative length or count, more than max_pages pages, dst not empty.  A request that is not granted changes nothing
+ *   (and fa_paged_append, given the same tokens and this status, writes nothing for it).
  * Table entries outside 0 .. num_pages - 1 in a part that is in use, and bad numbers in fa_pages_free, are skipped and
  * reported by fa_get_device_status as FA_ERR_INVALID.
  */
