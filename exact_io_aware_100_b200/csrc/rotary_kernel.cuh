@@ -56,6 +56,20 @@ __device__ __forceinline__ float rot_load(const T* p) { return static_cast<float
 template <typename T>
 __device__ __forceinline__ void rot_store(T* p, float x) { *p = static_cast<T>(x); }   // to nearest even
 
+// Packed offsets start at 0 or above, do not decrease and end at or below the number of rows.  The threads of the first
+// heads look at one each (or at every so many): a token looks up its own sequence only.
+template <bool APPEND>
+__device__ __forceinline__ void rot_check_offsets(const RotArgs& a) {
+  if constexpr (APPEND) {
+    if (a.cu == nullptr || blockIdx.y != 0) return;
+    const long long threads = static_cast<long long>(gridDim.x) * blockDim.x;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i <= a.B; i += threads) {
+      const int at = a.cu[i], before = i > 0 ? a.cu[i - 1] : 0;
+      if (at < before || at > a.total) atomicOr(a.status, DEV_ARGS);
+    }
+  }
+}
+
 // Where a token is: sequence, row within it, row coordinate in the tensors, position; the page row it goes to.
 struct RotToken {
   int b, row;
@@ -84,6 +98,7 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
         if (a.cu[mid] <= row) lo = mid; else hi = mid;
       }
       const int first = a.cu[lo], end = a.cu[lo + 1];
+      const int prev = lo > 0 ? a.cu[lo - 1] : first, next = lo + 2 <= a.B ? a.cu[lo + 2] : end;
       k.b = lo;
       k.row = row;
       k.pos = 0;
@@ -91,6 +106,8 @@ __device__ __forceinline__ RotToken rot_token(const RotArgs& a, long long t) {
       rows = end - first;
       if (row < first || row >= end) { k.skip = true; return k; }
       if (first < 0 || end > a.total) { atomicOr(a.status, DEV_ARGS); k.skip = true; return k; }
+      // out of order beside this sequence: its rows may be another's too (rot_check_offsets reports it)
+      if (prev > first || next < end) { k.skip = true; return k; }
     } else {
       k.b = static_cast<int>(t / a.N);
       k.row = static_cast<int>(t - static_cast<long long>(k.b) * a.N);
@@ -159,6 +176,7 @@ __device__ __forceinline__ float2 rot_turn(float xa, float xb, float2 cs) {
 template <typename T, bool APPEND>
 __global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a, int interleaved, int heads_per) {
   after_previous_kernel();
+  rot_check_offsets<APPEND>(a);
   const int half = a.r / 2, per = half + a.d - a.r;
   const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   const long long t = idx / per;
@@ -249,6 +267,7 @@ __global__ void __launch_bounds__(kRotThreads) fa_rotary_vec_kernel(const __grid
   using Word = typename R::Word;
   extern __shared__ __align__(16) uint8_t rot_smem[];
   after_previous_kernel();
+  rot_check_offsets<APPEND>(a);
   Word* buf = reinterpret_cast<Word*>(rot_smem) + threadIdx.x;   // [head][vector][thread]
   const int per = a.d / (2 * V), turning = a.r / (2 * V);      // items of a token, of which these turn
   const long long idx = static_cast<long long>(blockIdx.x) * kRotThreads + threadIdx.x;

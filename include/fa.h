@@ -324,7 +324,10 @@ typedef struct {
  * Without them every sequence gets n tokens: one that did not grow by n has
  * its last cached rows overwritten, on pages that others may share.
  * A packed row outside every sequence is not written either; its row of o is
- * zero, or what it was when o is q.  Two sequences must not receive tokens
+ * zero, or what it was when o is q.  Packed offsets have to start at 0 or above,
+ * not decrease, and end at or below total: what does not is reported by
+ * fa_get_device_status as FA_ERR_INVALID, and no row of a sequence with or next
+ * to such an offset is written.  Two sequences must not receive tokens
  * on the same page.  H is only used with q; H, H_kv < 2^16.
  */
 fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, void* k_pages, void* v_pages,

@@ -135,3 +135,55 @@ def test_counts_that_make_no_sense_are_reported():
         fa.paged_append(k, k, kp, vp, table, _i([9, 20, 30]), tokens=_i([2, bad, 1]), status=_i([0, 1, 0]))
         assert fa.fa_get_device_status() == fa.FA_OK                       # a refused sequence's count is not looked at
         assert torch.equal(kp, before)
+
+
+@pytest.mark.parametrize("r", [0, 64, 20])
+@pytest.mark.parametrize("cu,kept", [
+    ([0, 7, 3], []),                    # sequence 1 ends before it begins
+    ([0, 10, 4, 12], []),               # rows 4 to 9 belong to two sequences
+    ([0, 3, 9, 6, 12, 12], [0]),        # sequence 0 is not beside the place
+    ([0, 4, 4, 13], [0, 1]),            # more rows than there are
+    ([-1, 4, 12], [1]),
+    ([0, 12, 12, 5], [0]),              # no row looks at sequence 2
+    ([0, 12, 14, 14], [0]),             # sequences behind the last row
+    ([0, 5, 5, 12], [0, 1, 2]),         # in order: nothing to report
+])
+def test_packed_offsets_out_of_order_are_reported(cu, kept, r):
+    import torch
+    import exact_io_aware_100_b200 as fa
+    H, H_kv, d, page, total, B = 3, 2, 64, 8, 12, len(cu) - 1
+    lens = [20] * B
+    kp, vp = _cache(3 * B, H_kv, page, d)
+    table = torch.arange(3 * B, dtype=torch.int32, device="cuda").view(B, 3)
+    q, k, v = (torch.randn(total, h, d, device="cuda").bfloat16() for h in (H, H_kv, H_kv))
+    freqs = fa.rotary_frequencies(r)[0] if r else None
+    pos = torch.zeros(total, dtype=torch.int32, device="cuda")
+    real = torch.zeros(total, dtype=torch.bool, device="cuda")
+    for b in kept:
+        pos[cu[b]:cu[b + 1]] = torch.arange(20 - (cu[b + 1] - cu[b]), 20, dtype=torch.int32, device="cuda")
+        real[cu[b]:cu[b + 1]] = True
+    tq, tk = fa.rotary(q, k, freqs, pos) if r else (q, k)
+    rows = [(cu[b], cu[b + 1]) if b in kept else (0, 0) for b in range(B)]
+    hk, hv = ref.paged_append(to_f64(kp), to_f64(vp), table.cpu().numpy(), lens,
+                              [(to_f64(tk[x:y].transpose(0, 1)), to_f64(v[x:y].transpose(0, 1))) for x, y in rows])
+    got = fa.paged_append(k, v, kp, vp, table, _i(lens), q=q, freqs=freqs, cu_seqlens=_i(cu))
+    assert fa.fa_get_device_status() == (fa.FA_OK if len(kept) == B else fa.FA_ERR_INVALID)
+    assert np.array_equal(to_f64(kp), hk) and np.array_equal(to_f64(vp), hv)
+    assert torch.equal(got, tq.masked_fill(~real[:, None, None], 0.0))
+
+
+def test_packed_offsets_of_more_sequences_than_threads():
+    """One wrong offset among many sequences of one row or none."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    B = 5000
+    kp, vp = _cache(B, 1, 8, 64)
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    k = torch.randn(20, 1, 64, device="cuda").bfloat16()
+    cu = torch.arange(B + 1, device="cuda").clamp(max=20).int()
+    fa.paged_append(k, k, kp, vp, table, torch.ones(B, dtype=torch.int32, device="cuda"), cu_seqlens=cu)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    assert torch.equal(kp[:20, :, 0], k)
+    cu[4321] = 19
+    fa.paged_append(k, k, kp, vp, table, torch.ones(B, dtype=torch.int32, device="cuda"), cu_seqlens=cu)
+    assert fa.fa_get_device_status() == fa.FA_ERR_INVALID
