@@ -146,6 +146,13 @@ Tensor workspace_of(const Tensor* given, size_t bytes, const Tensor& like) {
   return given != nullptr ? *given : new_tensor({static_cast<int64_t>(bytes)}, at::kByte, like);
 }
 
+// A new output for rows like x's: in x's order of axes, d contiguous (which it would not be beside rows or heads that
+// overlap, one element apart).
+Tensor rows_like(const Tensor& x) {
+  Tensor y = at::empty_like(x);
+  return y.size(-1) <= 1 || y.stride(-1) == 1 ? y : new_tensor(x.sizes(), x.scalar_type(), x);
+}
+
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject* pair(PyObject* a, PyObject* b) {
   PyObject* t = PyTuple_New(2);
@@ -210,8 +217,8 @@ PyObject* rotary(PyObject* const* args, Py_ssize_t n) {
   {
     Unlocked u;
     Place place({&q, k, &freqs, positions, oq, ok});
-    q_out = oq != nullptr ? *oq : at::empty_like(q);
-    if (k != nullptr) k_out = ok != nullptr ? *ok : at::empty_like(*k);
+    q_out = oq != nullptr ? *oq : rows_like(q);
+    if (k != nullptr) k_out = ok != nullptr ? *ok : rows_like(*k);
     L.q = strides(&q);
     L.k = strides(k);
     L.q_out = strides(&q_out);
@@ -301,7 +308,7 @@ PyObject* paged_append(PyObject* const* args, Py_ssize_t n) {
     Unlocked u;
     Place place({&k, &v, &kp, &vp, &pt, &lens, q, freqs, cu, out, counts, status});
     if (out != nullptr) o = *out;
-    else if (q != nullptr) o = at::empty_like(*q);
+    else if (q != nullptr) o = rows_like(*q);
     L.q = strides(q);
     L.o = o ? strides(&*o) : fa_strides{0, 0, 0};
     L.k = strides(&k);
@@ -340,7 +347,7 @@ PyObject* paged_decode(PyObject* const* args, Py_ssize_t n) {
   {
     Unlocked u;
     Place place({&q, &kp, &vp, &pt, &lens, given});
-    o = at::empty_like(q);
+    o = rows_like(q);
     lse = new_tensor({L.B, L.H, L.N}, at::kFloat, q);
     L.q = strides(&q);
     L.o = strides(&o);

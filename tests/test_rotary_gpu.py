@@ -199,3 +199,23 @@ def test_rotary_gradient_is_the_transpose(interleaved):
         # two outputs of up to 8, each good to 1e-6 of |x_a| + |x_b| < 10, in two columns, times |dy| < 5, over h
         step = fa.rotary(x + e, None, freqs, pos, interleaved, 1.3)[0].double() - y.double()
         assert (((step * dy.double()).sum(-1) / h - dx[..., col].double()).abs() <= 4e-4).all()
+
+
+@pytest.mark.parametrize("size,stride", [
+    ((1, 1, 4, 64), (1, 1, 1, 1)),            # rows one element apart: windows over one line
+    ((2, 3, 5, 64), (7, 1, 100, 1)),          # heads one element apart
+    ((2, 3, 5, 64), (1, 64, 200, 1)),         # batch entries
+    ((2, 3, 5, 64), (0, 0, 3, 1)),
+    ((5, 3, 64), (1, 70, 1)),                 # packed rows
+])
+def test_rotary_of_overlapping_inputs(size, stride):
+    """Inputs may have any strides; the outputs made for them are tensors of their own, d contiguous."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    freqs, _ = fa.rotary_frequencies(64)
+    x = torch.randn(4096, device="cuda").bfloat16().as_strided(size, stride)
+    want = fa.rotary(x.contiguous(), x.contiguous(), freqs)
+    for f, want in ((fa.rotary, want), (fa.rotary_backward, fa.rotary_backward(x.contiguous(), x.contiguous(), freqs))):
+        got = f(x, x, freqs)
+        for g, w in zip(got, want):
+            assert g.stride(-1) == 1 and torch.equal(g, w)
