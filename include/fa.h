@@ -256,9 +256,11 @@ size_t fa_decode_workspace_size(int B, int H, int H_kv, int Lq, int Nk, int d);
  *  where the extent is above 1.  An output may be its input (same strides).
  *  positions: DEVICE int32, row n of batch entry b at positions[b *
  *  positions_batch + n]; NULL: row n has position n.  freqs: DEVICE double
- *  [rotary_dim / 2], radians per position, finite.  Angles are formed in fixed
- *  point as fractions of a turn, exact for every int32 position; products and
- *  sums are 32-bit, one rounding to dtype at the end.
+ *  [rotary_dim / 2], radians per position, finite, of either sign.  Angles are
+ *  formed in fixed point as fractions of a turn and reduced exactly; their error
+ *  is that of freqs / 2 pi in double (2^-52 relative) times the angle, and the
+ *  rounding of the reduced angle to 32 bits.  Products and sums are 32-bit, one
+ *  rounding to dtype at the end.
  * rotary_dim even, 0 <= rotary_dim <= d <= 1024 (FA_ERR_INVALID; d need not be
  * a multiple of 8).  B, H >= 1, N >= 0; B * N < 2^31; H, H_kv < 2^16.  Pointers are aligned to the element size
  * (FA_ERR_ALIGN).  Pointers and strides that are multiples of 16 bytes, with rotary_dim and d multiples of two such

@@ -219,3 +219,37 @@ def test_rotary_of_overlapping_inputs(size, stride):
         got = f(x, x, freqs)
         for g, w in zip(got, want):
             assert g.stride(-1) == 1 and torch.equal(g, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rotary_by_negative_frequencies_is_the_inverse_turn(dtype):
+    """The same angle with the other sign: the same bits."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    q, _ = _data(911, (2, 3, 40, 64), dtype)
+    pos = torch.arange(2**31 - 40, 2**31, dtype=torch.int64).int().cuda()
+    for f in (fa.rotary_frequencies(64)[0], torch.logspace(-18, -6, 32, dtype=torch.float64, device="cuda")):
+        for interleaved in (False, True):
+            for p in (pos, -pos):
+                a, _ = fa.rotary(q, None, -f, p, interleaved, 1.5)
+                b, _ = fa.rotary_backward(q, None, f, p, interleaved, 1.5)
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rotary_small_angles_of_far_positions(sign):
+    """x_a = 0, x_b = 1: y_a = -sin t, for t from 2e-9 to 2e3.  The fraction of a turn is cut to 2^-32, after a product with a
+    step that is cut to 2^-64 and taken up to 2^31 times (2^-33): 2 pi (2^-32 + 2^-33) = 2.2e-9 rad.  It is rounded to 2^-24 of
+    itself; the sine has two steps, freqs / 2 pi 2^-52 of t."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    f = sign * 10.0 ** np.linspace(-18, -6, 32)
+    x = torch.zeros(1, 1, 64, 64, device="cuda")
+    x[..., 32:] = 1.0
+    pos = np.arange(2**31 - 64, 2**31)
+    y, _ = fa.rotary(x, None, torch.tensor(f, device="cuda"), torch.from_numpy(pos).int().cuda())
+    t = pos[:, None].astype(np.longdouble) * f.astype(np.longdouble)
+    want = -np.sin(t)
+    small = np.minimum(np.abs(t), np.pi)             # the reduced angle is no further out
+    bound = 2 * np.pi * (2.0 ** -32 + 2.0 ** -33) + small * 2.0 ** -24 + np.abs(want) * 2.0 ** -22 + np.abs(t) * 2.0 ** -52
+    assert (np.abs(to_f64(y)[0, 0, :, :32] - want) <= bound).all()
