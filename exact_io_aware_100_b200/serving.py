@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import os
 
 import exact_io_aware_100_b200 as _fa
 
@@ -155,7 +156,9 @@ def _native():
         try:
             from . import _serving
         except ImportError as e:
-            raise RuntimeError("_serving.so is not built; run `python -m exact_io_aware_100_b200.build`") from e
+            from . import build
+            what = "does not load with this Python and torch" if os.path.exists(build.EXT) else "is not built"
+            raise RuntimeError(f"_serving.so {what} ({e}); run `python -m exact_io_aware_100_b200.build`") from e
         L = _fa.load_library()
         _serving.bind(_fa.FaError, *(ctypes.cast(getattr(L, name), _VP).value for name in (
             "fa_rotary", "fa_paged_append", "fa_paged_decode", "fa_paged_decode_workspace_size", "fa_pages_workspace_size",
