@@ -25,10 +25,12 @@
 //  * the products are warp-level matrix instructions (16 rows x 8 columns x 16): rows
 //    are few, and the tcgen05 tiles start at 64 rows.  S = Q K^T gives its accumulators
 //    in the layout that P V wants its left operand in, so P stays in registers;
-//  * P is rounded to bf16 for the second product; with at most 8 rows its remainder rides
-//    in the 8 unused rows of the same instruction, which makes it 16 bits of mantissa.
-//    (With more rows the remainder would take a second instruction.)  Everything else
-//    is 32-bit; O is rounded once.
+//  * P enters the second product as a bf16 and the bf16 of what that rounding left, 16 bits
+//    of mantissa, however many rows there are and however a call is cut.  In tiles of 8 rows
+//    the remainder rides in the 8 unused rows of the same instruction, in higher ones it
+//    takes a second one (32 rows, d 64, 1.07 GB of cache: 182 us without, 211 with it;
+//    16 rows, d 128, 0.54 GB: 101 and 103).
+//    Everything else is 32-bit; O is rounded once.
 //  * O is rescaled only when a row's maximum grows by more than 2^8.
 #pragma once
 
@@ -73,7 +75,7 @@ __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
   return n;
 }
 
-// D: head dim.  RM: query rows of a row tile (8, 16 or 32).
+// D: head dim.  RM: query rows of a row tile (8, 16 or, d 64, 32).
 template <int D_, int RM_>
 struct PagedCfg {
   static constexpr int D = D_, RM = RM_;
@@ -99,13 +101,18 @@ constexpr int kPagedMinUnits = 2;                // of a range: what is in fligh
 // How pairs whose table rows hold `tiles` tiles at most are shared out: each to a warp, each to a block's four warps, or
 // cut into ranges of equal length.  Uncut pairs take no planning, no partials and no second launch, but one warp's (or
 // four warps') time for their tiles.  Measured (device time, us; warp / block / cut; rows R per key/value head):
-//   8 pairs, d 128, R 4:     1 tile 3.9 / - / 7.0, 4 tiles 6.3 / - / 8.5, 8 tiles - / 4.8 / 9.1, 32 tiles - / 9.4 / 9.7,
-//                            64 tiles - / 15.8 / 10.6
-//   128 pairs:               8 tiles 10.0 / 5.1 / 10.6, 16 tiles 16.4 / 6.7 / 11.2, 64 tiles - / 16.5 / 17.4
-//   512 pairs:               8 tiles 9.7 / 11.2 / -, 16 tiles 16.3 / 14.8 / 21, 32 tiles - / 28 / 34
-//   1024 pairs:              16 tiles 25.5 / - / 34.5
-//   4 pairs, d 256, R 16:    8 tiles - / 11.4 / 13.3, 16 tiles - / 15.5 / 13.4;  64 pairs: 16 tiles - / 15.6 / 20.1;
-//                            256 pairs: 64 tiles - / 53 / 71
+//   8 pairs, d 128, R 4:     1 tile 4.0 / 4.0 / 7.2, 2 tiles 4.7 / 4.1 / 7.5, 20 tiles 19.1 / 7.4 / 9.5, 32 tiles 28 / 9.4 / 9.4,
+//                            36 tiles 32 / 10.4 / 9.6;  d 64: 28 tiles 29 / 9.3 / 9.3, 36 tiles 36 / 11.1 / 9.5
+//   8 pairs, d 256, R 8:     16 tiles 24 / 9.6 / 10.4, 20 tiles 29 / 11.0 / 11.3, 24 tiles 34 / 12.0 / 11.2
+//   64 pairs, d 128, R 4:    32 tiles 29 / 9.9 / 12.0, 40 tiles 36 / 11.7 / 12.7, 48 tiles 42 / 13.2 / 13.3
+//   64 pairs, d 256, R 8:    24 tiles 34 / 12.5 / 13.7, 32 tiles 44 / 15.0 / 13.9;  32 pairs: 24 tiles 33 / 12.5 / 11.9
+//   136 pairs, d 128, R 4:   64 tiles 56 / 16.5 / 17.5, 80 tiles 69 / 20.1 / 19.8;  192 pairs: 64 tiles 56 / 20.1 / 22.8
+//   320 pairs:               12 tiles 12.8 / 12.3 / 13.3, 16 tiles 16.0 / 14.1 / 14.3, 64 tiles 56 / 42 / 38
+//   480 pairs:               12 tiles 13.0 / 13.0 / 16.9, 16 tiles 16.2 / 14.8 / 18.7, 64 tiles 57 / 45 / 52
+//   640 pairs:               16 tiles 18.4 / 21 / 19.5, 20 tiles 23.4 / 26 / 24.8;  1280: 16 tiles 36 / 40 / 38, 24 tiles 50 / 53 / 52
+//   16-row tiles (pairs times row tiles): 12, d 128: 20 tiles 22 / 10.2 / 10.8, 28 tiles 29 / 11.8 / 10.9;  d 64: 20 tiles
+//                            25 / 10.1 / 10.2, 24 tiles 29 / 11.1 / 10.4;  d 256: 12 tiles 33 / 14.1 / 14.9, 16 tiles 42 / 16.4 / 15.2
+//   96, d 256:               24 tiles 61 / 21 / 23.5, 32 tiles 80 / 26 / 24;  48, d 256: 24 tiles 61 / 21 / 20.4
 enum PagedShare { kPagedCut, kPagedByWarp, kPagedByBlock };
 inline PagedShare paged_share(int d, int rm, long long pairs, long long tiles) {
   const bool joins = rm <= 16;                     // blocks join their warps' parts up to 16 rows
@@ -120,17 +127,25 @@ inline PagedShare paged_share(int d, int rm, long long pairs, long long tiles) {
 constexpr int kPagedTeam = 32;
 constexpr int kPagedPairUnits = 2;               // what beginning and ending a pair costs, in tiles
 
-// Rows of a row tile: 8, 16 or (d < 256) 32.  Small row tiles read every key several times, but once only from HBM, and take
-// a warp less time per tile: what counts while calls are short and blocks fit the GPU at once.  `tiles` are those of all
-// pairs.  Device time, us, by the rows of a tile:
-//   16 rows, d 256, 4 pairs of 8 tiles (8 / 16) 7.4 / 10.8, of 256 tiles 16.5 / 18.2; 64 pairs of 64 tiles 25.5 / 25.7
-//   16 rows, d 128, 64 pairs of 8 tiles 5.7 / 7.3, of 32 tiles 10.6 / 12.3, of 256 tiles 39.7 / 36.6; 256 pairs of 8 10.0 / 8.1
-//   32 rows, d 128, 64 pairs of 64 tiles (16 / 32) 21 / 24, of 256 tiles 42 / 52, of 1024 tiles 130 / 121
-//   24 rows, d 64, 2 pairs of 8 tiles 6.3 / 10.3, 32 pairs of 32 tiles 12.4 / 14.0, of 128 tiles 19.4 / 17.7
+// Rows of a row tile: 8, 16 or (d 64) 32.  Small row tiles read every key several times, but once only from HBM, and take
+// a warp less time per tile: what counts while calls are short and blocks fit the GPU at once.  With d 256, 17 to 24 rows
+// fill three tiles of 8 and leave half of a second tile of 16 empty.  `tiles` are those of all pairs.  Device time, us, by
+// the rows of a tile (8 / 16, d 64 and 128: / 32):
+//   16 rows, d 128, 4 pairs of 64 tiles 11.4 / 12.7 / 14; 64 pairs of 32 tiles 10.9 / 12.9 / 19, of 128 27 / 22.6 / 32;
+//                   256 pairs of 4 tiles 7.0 / 7.8 / 12, of 8 10.2 / 9.1 / 21
+//   32 rows, d 128, 64 pairs of 32 tiles 12.7 / 13.1 / 24, of 256 64 / 44 / 53, of 1024 215 / 130 / 136; 256 pairs of 256 216 / 131 / 139
+//   64 rows, d 128, 64 pairs of 1024 tiles - / 243 / 242; 256 pairs of 64 - / 78 / 86, of 256 - / 247 / 250
+//                   (32 rows of d 128 take 255 registers and spill: they win nowhere, and no such kernel is built)
+//   24 rows, d 64, 32 pairs of 64 tiles 16.4 / 16.0 / 15.8, of 128 22.1 / 20.8 / 19.4, of 1024 100 / 81 / 64; 256 pairs of 8
+//                   12.0 / 12.2 / 16, of 32 34 / 28 / 26
+//   16 rows, d 256, 4 pairs of 256 tiles 17.1 / 19.6; 64 pairs of 256 61 / 70, of 1024 197 / 192; 256 pairs of 32 46 / 33
+//   32 rows, d 256, 32 pairs of 256 tiles 56 / 58, of 1024 176 / 164; 64 pairs of 256 96 / 94
+//   24 rows, d 256, 4 pairs of 1024 tiles 31 / 36; 64 pairs of 256 77 / 93; 256 pairs of 4 11.3 / 15.7, of 256 261 / 324
 inline int paged_row_tile(int d, int rows, long long pairs, long long tiles) {
   const int eights = (rows + 7) / 8;
-  if (eights == 1 || (eights <= 4 && pairs * eights < 2 * 148 && tiles <= (d == 256 ? 4 : 2) * 1184LL)) return 8;
-  return rows <= 16 || d == 256 || tiles <= (d == 64 ? 2 : 14) * 1184LL ? 16 : 32;
+  if (eights == 1 || (d == 256 && eights == 3)) return 8;
+  if (eights <= 4 && pairs * eights < 2 * 148 && tiles <= (d == 256 ? 14 : 2) * 1184LL) return 8;
+  return rows <= 16 || d > 64 || tiles <= 2 * 1184LL ? 16 : 32;
 }
 // Warps that share one row tile's work.
 __host__ __device__ inline int paged_workers(int row_tiles) {
@@ -473,6 +488,7 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
   if (!busy)
     for (int rr = lane; rr < RM; rr += 32) team_ml[warp * RM + rr] = make_float2(-INFINITY, 0.f);
   uint32_t p[MT][NT / 2][4];                       // per 16 keys: keys 0 .. 7 (rows, rows + 8), then keys 8 .. 15
+  uint32_t lo[C::HALF ? 1 : MT][C::HALF ? 1 : NT / 2][4];   // what p's rounding left (HALF: in p's rows 8 .. 15)
 #pragma unroll 1
   for (int ahead = C::SLOTS - 1; busy;) {          // tiles to load before the first is used
     if (ahead == 0) {
@@ -583,11 +599,16 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         for (int n = 0; n < NT; ++n) {
           uint32_t* y = &p[mt][n / 2][2 * (n % 2)];
           y[0] = pack_bf16x2(s[mt][n][0], s[mt][n][1]);
+          const float2 h = bf16x2_to_float2(y[0]);
+          const uint32_t left = pack_bf16x2(s[mt][n][0] - h.x, s[mt][n][1] - h.y);
           if constexpr (C::HALF) {
-            const float2 h = bf16x2_to_float2(y[0]);
-            y[1] = pack_bf16x2(s[mt][n][0] - h.x, s[mt][n][1] - h.y);
+            y[1] = left;
           } else {
             y[1] = pack_bf16x2(s[mt][n][2], s[mt][n][3]);
+            const float2 g = bf16x2_to_float2(y[1]);
+            uint32_t* z = &lo[mt][n / 2][2 * (n % 2)];
+            z[0] = left;
+            z[1] = pack_bf16x2(s[mt][n][2] - g.x, s[mt][n][3] - g.y);
           }
         }
       second = C::SPLIT;
@@ -618,6 +639,11 @@ fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
           const uint32_t* y = p[mt][kk];
           mma_bf16(acc[mt][n], y[0], y[1], y[2], y[3], vf[0], vf[1]);
           mma_bf16(acc[mt][n + 1], y[0], y[1], y[2], y[3], vf[2], vf[3]);
+          if constexpr (!C::HALF) {
+            const uint32_t* z = lo[mt][kk];
+            mma_bf16(acc[mt][n], z[0], z[1], z[2], z[3], vf[0], vf[1]);
+            mma_bf16(acc[mt][n + 1], z[0], z[1], z[2], z[3], vf[2], vf[3]);
+          }
         }
       }
     const bool ends = at.tile + 1 == at.tiles, stop = at.unit + 1 + (ends ? at.gap(a) : 0) >= t1;

@@ -401,9 +401,9 @@ fa_status fa_paged_decode(const void* q, const void* k_pages, const void* v_page
     case 2: return launch_paged<64, 32>(tk, tv, a, attr, s);
     case 3: return launch_paged<128, 8>(tk, tv, a, attr, s);
     case 4: return launch_paged<128, 16>(tk, tv, a, attr, s);
-    case 5: return launch_paged<128, 32>(tk, tv, a, attr, s);
     case 6: return launch_paged<256, 8>(tk, tv, a, attr, s);
-    default: return launch_paged<256, 16>(tk, tv, a, attr, s);
+    case 7: return launch_paged<256, 16>(tk, tv, a, attr, s);
+    default: return FA_ERR_UNSUPPORTED;              // (32 rows of d 128 or 256: paged_row_tile gives none)
   }
 }
 

@@ -345,8 +345,7 @@ fa_status fa_paged_append(const void* q, const void* k, const void* v, void* o, 
  * seq_lens[b]) gets o = 0, lse = -inf.  H a multiple of H_kv; N >= 1, H / H_kv * N < 2^19.  What
  * the pages hold behind a sequence's end does not matter (NaN included); a key
  * that only some of the N queries see has to be finite.  Scores, softmax and sums
- * are 32-bit; the probabilities enter the second product with 16 bits of mantissa
- * when H / H_kv * N <= 8 (and in some short calls with more), else rounded to bf16;
+ * are 32-bit; the probabilities enter the second product with 16 bits of mantissa;
  * o is rounded once.
  * workspace: at least fa_paged_decode_workspace_size(layout) bytes, 256-byte
  * aligned; not shared by calls that may overlap.
