@@ -8,6 +8,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <ATen/ops/full.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -46,6 +47,7 @@ struct Failed {
 void check(fa_status code, const char* where) {
   if (code != FA_OK) throw Failed{code, where};
 }
+// The library wants one sequence at least; a call on none (and, decode, on no rows) gives empty outputs and does not reach it.
 
 struct Unlocked {                  // the interpreter may run other threads while a call allocates and launches
   PyThreadState* state = PyEval_SaveThread();
@@ -223,10 +225,11 @@ PyObject* rotary(PyObject* const* args, Py_ssize_t n) {
     L.k = strides(k);
     L.q_out = strides(&q_out);
     L.k_out = k_out ? strides(&*k_out) : fa_strides{0, 0, 0};
-    check(lib.rotary(data<void>(q), data<void>(k), data<void>(q_out), k_out ? data<void>(*k_out) : nullptr,
-                     data<int32_t>(positions), data<double>(freqs), &L, static_cast<float>(magnitude), inverse,
-                     q.scalar_type() == at::kBFloat16 ? FA_BF16 : FA_F32, place.stream),
-          "fa_rotary");
+    if (L.B != 0)
+      check(lib.rotary(data<void>(q), data<void>(k), data<void>(q_out), k_out ? data<void>(*k_out) : nullptr,
+                       data<int32_t>(positions), data<double>(freqs), &L, static_cast<float>(magnitude), inverse,
+                       q.scalar_type() == at::kBFloat16 ? FA_BF16 : FA_F32, place.stream),
+            "fa_rotary");
   }
   if (oq != nullptr) {               // the caller's own tensors, not views of them
     PyObject *a = PyTuple_GET_ITEM(args[6], 0), *b = PyTuple_GET_ITEM(args[6], 1);
@@ -316,10 +319,11 @@ PyObject* paged_append(PyObject* const* args, Py_ssize_t n) {
     L.cu_seqlens = data<int32_t>(cu);
     L.tokens = data<int32_t>(counts);
     L.status = data<int32_t>(status);
-    check(lib.paged_append(data<void>(q), data<void>(k), data<void>(v), o ? data<void>(*o) : nullptr, data<void>(kp),
-                           data<void>(vp), data<int32_t>(pt), data<int32_t>(lens), data<double>(freqs), &L,
-                           static_cast<float>(magnitude), place.stream),
-          "fa_paged_append");
+    if (L.B != 0 || L.total != 0)
+      check(lib.paged_append(data<void>(q), data<void>(k), data<void>(v), o ? data<void>(*o) : nullptr, data<void>(kp),
+                             data<void>(vp), data<int32_t>(pt), data<int32_t>(lens), data<double>(freqs), &L,
+                             static_cast<float>(magnitude), place.stream),
+            "fa_paged_append");
   }
   if (out != nullptr) {
     Py_INCREF(args[11]);
@@ -351,11 +355,13 @@ PyObject* paged_decode(PyObject* const* args, Py_ssize_t n) {
     lse = new_tensor({L.B, L.H, L.N}, at::kFloat, q);
     L.q = strides(&q);
     L.o = strides(&o);
-    const Tensor ws = workspace_of(given, lib.paged_decode_workspace_size(&L), q);
-    check(lib.paged_decode(data<void>(q), data<void>(kp), data<void>(vp), data<int32_t>(pt), data<int32_t>(lens),
-                           data<void>(o), data<float>(lse), &L, static_cast<float>(scale), causal, data<void>(ws),
-                           ws.nbytes(), place.stream),
-          "fa_paged_decode");
+    if (L.B != 0 && L.N != 0) {
+      const Tensor ws = workspace_of(given, lib.paged_decode_workspace_size(&L), q);
+      check(lib.paged_decode(data<void>(q), data<void>(kp), data<void>(vp), data<int32_t>(pt), data<int32_t>(lens),
+                             data<void>(o), data<float>(lse), &L, static_cast<float>(scale), causal, data<void>(ws),
+                             ws.nbytes(), place.stream),
+            "fa_paged_decode");
+    }
   }
   return pair(wrap(std::move(o)), wrap(std::move(lse)));
 }
@@ -392,10 +398,12 @@ PyObject* pages_extend(PyObject* const* args, Py_ssize_t n) {
     Unlocked u;
     Place place({&pt, &lens, &refs, &seqs, &tokens, given});
     status = new_tensor({count}, at::kInt, seqs);
-    const Tensor ws = workspace_of(given, lib.pages_workspace_size(&L, count), seqs);
-    check(lib.pages_extend(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(seqs),
-                           data<int32_t>(tokens), count, data<int32_t>(status), data<void>(ws), ws.nbytes(), place.stream),
-          "fa_pages_extend");
+    if (L.num_seqs != 0 || count != 0) {
+      const Tensor ws = workspace_of(given, lib.pages_workspace_size(&L, count), seqs);
+      check(lib.pages_extend(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(seqs),
+                             data<int32_t>(tokens), count, data<int32_t>(status), data<void>(ws), ws.nbytes(), place.stream),
+            "fa_pages_extend");
+    }
   }
   return wrap(std::move(status));
 }
@@ -414,11 +422,13 @@ PyObject* pages_fork(PyObject* const* args, Py_ssize_t n) {
     Place place({&pt, &lens, &refs, &src, &dst, given});
     copies = new_tensor({count, 3}, at::kInt, src);
     status = new_tensor({count}, at::kInt, src);
-    const Tensor ws = workspace_of(given, lib.pages_workspace_size(&L, count), src);
-    check(lib.pages_fork(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(src),
-                         data<int32_t>(dst), count, data<int32_t>(copies), data<int32_t>(status), data<void>(ws),
-                         ws.nbytes(), place.stream),
-          "fa_pages_fork");
+    if (L.num_seqs != 0 || count != 0) {
+      const Tensor ws = workspace_of(given, lib.pages_workspace_size(&L, count), src);
+      check(lib.pages_fork(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(src),
+                           data<int32_t>(dst), count, data<int32_t>(copies), data<int32_t>(status), data<void>(ws),
+                           ws.nbytes(), place.stream),
+            "fa_pages_fork");
+    }
   }
   return pair(wrap(std::move(copies)), wrap(std::move(status)));
 }
@@ -433,9 +443,10 @@ PyObject* pages_free(PyObject* const* args, Py_ssize_t n) {
   {
     Unlocked u;
     Place place({&pt, &lens, &refs, &seqs});
-    check(lib.pages_free(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(seqs),
-                         extent(seqs.size(0)), place.stream),
-          "fa_pages_free");
+    if (L.num_seqs != 0 || seqs.size(0) != 0)
+      check(lib.pages_free(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(seqs),
+                           extent(seqs.size(0)), place.stream),
+            "fa_pages_free");
   }
   Py_RETURN_NONE;
 }
@@ -450,11 +461,15 @@ PyObject* pages_compact(PyObject* const* args, Py_ssize_t n) {
   {
     Unlocked u;
     Place place({&pt, &lens, &refs, given});
-    copies = new_tensor({L.num_pages / 2, 3}, at::kInt, refs);
-    const Tensor ws = workspace_of(given, lib.pages_workspace_size(&L, 0), refs);
-    check(lib.pages_compact(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(copies),
-                            data<void>(ws), ws.nbytes(), place.stream),
-          "fa_pages_compact");
+    if (L.num_seqs == 0) {
+      copies = at::full({L.num_pages / 2, 3}, -1, refs.options());
+    } else {
+      copies = new_tensor({L.num_pages / 2, 3}, at::kInt, refs);
+      const Tensor ws = workspace_of(given, lib.pages_workspace_size(&L, 0), refs);
+      check(lib.pages_compact(data<int32_t>(pt), data<int32_t>(lens), data<int32_t>(refs), &L, data<int32_t>(copies),
+                              data<void>(ws), ws.nbytes(), place.stream),
+            "fa_pages_compact");
+    }
   }
   return wrap(std::move(copies));
 }

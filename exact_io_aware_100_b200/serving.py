@@ -19,6 +19,7 @@ reads ``status``, makes room for the refused (frees or moves sequences) and give
 
 Tensors may live on any CUDA device; a call runs on their device, on that device's current stream or on
 ``stream``.  With ``stream`` the outputs are allocated on it and the inputs are recorded as in use there.
+A call on no sequences or no rows returns empty tensors.
 """
 from __future__ import annotations
 

@@ -187,3 +187,44 @@ def test_packed_offsets_of_more_sequences_than_threads():
     cu[4321] = 19
     fa.paged_append(k, k, kp, vp, table, torch.ones(B, dtype=torch.int32, device="cuda"), cu_seqlens=cu)
     assert fa.fa_get_device_status() == fa.FA_ERR_INVALID
+
+
+def test_no_sequences_and_no_rows():
+    """A batch that has run empty goes through the same calls."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    kp, vp = _cache(6, 2, 8, 64)
+    before = kp.clone()
+    new = lambda *shape: torch.zeros(*shape, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    freqs, _ = fa.rotary_frequencies(64)
+    none, refs = _i([]), _i([0, 1, 0, 0, 0, 0])
+    table = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    book = (table, none, refs, 8)
+    for n in (1, 0, 5):
+        q, k = new(0, 4, n, 64), new(0, 2, n, 64)
+        got = fa.rotary(q, k, freqs)
+        assert got[0].shape == q.shape and got[1].shape == k.shape
+        got = fa.paged_append(k, k, kp, vp, table, none, q=q, freqs=freqs, tokens=none, status=none)
+        assert got.shape == q.shape
+        o, lse = fa.paged_decode(q, kp, vp, table, none)
+        assert o.shape == q.shape and lse.shape == (0, 4, n) and lse.dtype == torch.float32
+    got = fa.paged_append(new(0, 2, 64), new(0, 2, 64), kp, vp, table, none, q=new(0, 4, 64), cu_seqlens=_i([0]))
+    assert got.shape == (0, 4, 64)
+    assert fa.pages_extend(*book, none, none).shape == (0,)
+    copies, status = fa.pages_fork(*book, none, none)
+    assert copies.shape == (0, 3) and status.shape == (0,)
+    fa.pages_free(*book, none)
+    assert fa.pages_compact(*book).tolist() == [[-1] * 3] * 3 and refs.tolist() == [0, 1, 0, 0, 0, 0]
+    fa.pages_copy(kp, vp, torch.empty(0, 3, dtype=torch.int32, device="cuda"))
+    # one sequence, no rows
+    one, lens = torch.zeros(1, 3, dtype=torch.int32, device="cuda"), _i([4])
+    o, lse = fa.paged_decode(new(1, 4, 0, 64), kp, vp, one, lens)
+    assert o.shape == (1, 4, 0, 64) and lse.shape == (1, 4, 0)
+    assert fa.paged_append(new(1, 2, 0, 64), new(1, 2, 0, 64), kp, vp, one, lens, q=new(1, 4, 0, 64)).shape == (1, 4, 0, 64)
+    torch.cuda.synchronize()
+    assert torch.equal(kp, before) and fa.fa_get_device_status() == fa.FA_OK
+    # what makes no sense is refused as before: rows or requests of no sequence
+    with pytest.raises(fa.FaError):
+        fa.paged_append(new(3, 2, 64), new(3, 2, 64), kp, vp, table, none, cu_seqlens=_i([0]))
+    with pytest.raises(fa.FaError):
+        fa.pages_extend(*book, _i([0]), _i([1]))
