@@ -110,6 +110,9 @@ constexpr int kPagedMinUnits = 2;                // of a range: what is in fligh
 //   320 pairs:               12 tiles 12.8 / 12.3 / 13.3, 16 tiles 16.0 / 14.1 / 14.3, 64 tiles 56 / 42 / 38
 //   480 pairs:               12 tiles 13.0 / 13.0 / 16.9, 16 tiles 16.2 / 14.8 / 18.7, 64 tiles 57 / 45 / 52
 //   640 pairs:               16 tiles 18.4 / 21 / 19.5, 20 tiles 23.4 / 26 / 24.8;  1280: 16 tiles 36 / 40 / 38, 24 tiles 50 / 53 / 52
+//   32-row tiles, d 64 (no joining): 320 pairs: 12 tiles 21.3 / - / 20.3, 16 tiles 26.8 / - / 22.1;  480: 16 tiles 27 / - / 30,
+//                            20 tiles 32.9 / - / 32.8;  640: 16 tiles 33 / - / 37, 20 tiles 41 / - / 41
+//   16-row tiles, d 128:     320 pairs: 12 tiles 15.0 / 16.9 / 15.6;  480: 12 tiles 15 / 18 / 19, 64 tiles 64 / 52 / 57
 //   16-row tiles (pairs times row tiles): 12, d 128: 20 tiles 22 / 10.2 / 10.8, 28 tiles 29 / 11.8 / 10.9;  d 64: 20 tiles
 //                            25 / 10.1 / 10.2, 24 tiles 29 / 11.1 / 10.4;  d 256: 12 tiles 33 / 14.1 / 14.9, 16 tiles 42 / 16.4 / 15.2
 //   96, d 256:               24 tiles 61 / 21 / 23.5, 32 tiles 80 / 26 / 24;  48, d 256: 24 tiles 61 / 21 / 20.4
@@ -118,7 +121,7 @@ inline PagedShare paged_share(int d, int rm, long long pairs, long long tiles) {
   const bool joins = rm <= 16;                     // blocks join their warps' parts up to 16 rows
   if (pairs < 2 * 148) {
     const int few = pairs >= 32 ? (rm == 16 && d == 256 ? 24 : 32) : d == 256 ? (rm == 8 ? 20 : 12) : rm == 8 ? 32 : 20;
-    if (tiles <= (joins ? 1 : 4)) return kPagedByWarp;
+    if (tiles <= 1) return kPagedByWarp;
     return joins && tiles <= (pairs < 128 ? few : 64) ? kPagedByBlock : kPagedCut;
   }
   if (tiles <= (pairs < 4 * 148 && joins ? 12 : 16)) return kPagedByWarp;

@@ -257,8 +257,8 @@ __device__ __forceinline__ void rot_fetch(void* dst, const void* src) {
 
 // The vector path: aligned rows whose turned columns fall into whole pairs of vectors of V elements (half layout: r a
 // multiple of 2 V), or into whole vectors (interleaved: of V); d a multiple of 2 V.  A thread takes two vectors of a token
-// in up to kRotHeads heads: it asks for all of them (through shared memory, where they cost no registers: 32 KB a block,
-// up to 224 KB an SM in flight), forms the angles meanwhile, once for all heads, and turns and writes head by head.  It
+// in up to kRotHeads heads: it asks for all of them (through shared memory, where they cost no registers: 32 KB a block; with
+// 40, 48 and 58 registers (fp32, bf16, append) 6, 5 and 4 blocks to an SM, 192, 160 and 128 KB in flight), forms the angles meanwhile, once for all heads, and turns and writes head by head.  It
 // reads what it fetched itself: no barrier.  Training shape (2 x 40 heads x 8192 x 128, forward and backward): 109 us with
 // 4 heads, 110 with 6, 112 with 8; 120 with four heads in flight in registers, 131 with angles shared through a block
 // barrier; 111 with the fetches asked for before the token's look-ups (append of prompts 61.6 -> 63.8).
