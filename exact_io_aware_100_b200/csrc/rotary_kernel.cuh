@@ -41,16 +41,23 @@ struct RotArgs {
   uint32_t* status;
 };
 
-// cos and sin (times the magnitude) of the angle pos * f.
+// cos and sin (times the magnitude) of the angle pos * f.  FINE (32-bit outputs): the nearest quarter turn comes off as an
+// integer first, so that what is rounded to 32 bits is an eighth of a turn at most and not half a one.  (Error of 32-bit
+// outputs, relative 2-norm: 4.4e-8 -> 3.4e-8; with 3.2e-8 from sines in 64 bits.  Outputs in bf16 do not show it, and the
+// selections took append of prompts from 62.8 to 66.6 us.)
+template <bool FINE>
 __device__ __forceinline__ float2 rot_cos_sin(double f, int pos, float magnitude, int inverse) {
   const double turn = fabs(f) * 0.15915494309189535;             // |f| / 2 pi (1 - |turn| would round a small one away)
   const bool back = (inverse != 0) != (__double2hiint(f) < 0);
   const unsigned long long step = __double2ull_rz((turn - floor(turn)) * 18446744073709551616.0);
   const long long where = static_cast<long long>(step * static_cast<unsigned long long>(static_cast<long long>(pos)));
-  const float half_turns = static_cast<float>(static_cast<int>(where >> 32)) * 4.656612873077393e-10f;   // 2^-31
+  const unsigned at = static_cast<unsigned>(where >> 32), quarters = FINE ? (at + (1u << 29)) >> 30 : 0u;
+  const float half_turns = static_cast<float>(static_cast<int>(at - (quarters << 30))) * 4.656612873077393e-10f;   // 2^-31
   float s, c;
   sincospif(half_turns, &s, &c);
-  return make_float2(__fmul_rn(c, magnitude), __fmul_rn(back ? -s : s, magnitude));
+  const float x = quarters & 1 ? s : c, y = quarters & 1 ? c : s;
+  return make_float2(__fmul_rn((quarters + 1) & 2 ? -x : x, magnitude),
+                     __fmul_rn(((quarters & 2) != 0) != back ? -y : y, magnitude));
 }
 
 template <typename T>
@@ -187,7 +194,7 @@ __global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a, int int
   const RotToken tk = rot_token<APPEND>(a, t);
   const bool turn = p < half;
   const int ca = turn ? (interleaved ? 2 * p : p) : p + half, cb = turn ? (interleaved ? 2 * p + 1 : p + half) : ca;
-  const float2 cs = turn ? rot_cos_sin(a.freqs[p], tk.pos, a.magnitude, a.inverse) : make_float2(1.f, 0.f);
+  const float2 cs = turn ? rot_cos_sin<sizeof(T) == 4>(a.freqs[p], tk.pos, a.magnitude, a.inverse) : make_float2(1.f, 0.f);
   const bool pad = APPEND && (tk.skip || tk.page < 0);
   const int heads = pad ? (tk.skip && a.qo == a.q ? 0 : a.H) : a.H + (APPEND ? 2 : 1) * a.H_kv;
   const int h1 = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per);
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kRotThreads) fa_rotary_vec_kernel(const __grid
   for (int e = 0; e < V; ++e)
     if (e < V / 2 ? turn_a : turn_b) {
       const int pair = INTER ? (e < V / 2 ? ca : cb - V) / 2 + e : ca + e;
-      cs[e] = rot_cos_sin(a.freqs[pair], tk.pos, a.magnitude, a.inverse);
+      cs[e] = rot_cos_sin<sizeof(T) == 4>(a.freqs[pair], tk.pos, a.magnitude, a.inverse);
     }
   asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1

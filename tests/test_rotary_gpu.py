@@ -253,3 +253,26 @@ def test_rotary_small_angles_of_far_positions(sign):
     small = np.minimum(np.abs(t), np.pi)             # the reduced angle is no further out
     bound = 2 * np.pi * (2.0 ** -32 + 2.0 ** -33) + small * 2.0 ** -24 + np.abs(want) * 2.0 ** -22 + np.abs(t) * 2.0 ** -52
     assert (np.abs(to_f64(y)[0, 0, :, :32] - want) <= bound).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_float32_angles(interleaved):
+    """x_a = 1, x_b = 0: y = (cos t, sin t) all around the turn.  The reduced angle, an eighth of a turn at most once the
+    nearest quarter is off, is rounded to 2^-24 of itself (half of pi / 4's step: pi 2^-27) and cut to 2^-32 of a turn;
+    freqs / 2 pi adds 2^-52 of t, and the sine or cosine two steps.  An angle rounded as half a turn would be off by pi 2^-25."""
+    import torch
+    import exact_io_aware_100_b200 as fa
+    f = np.array([0.001, 0.37, 1.0, 1.5707963, 2.9])
+    x = torch.zeros(1, 1, 40000, 10, device="cuda")
+    x[..., 0::2 if interleaved else 1] = 1.0
+    if not interleaved:
+        x[..., 5:] = 0.0
+    y, _ = fa.rotary(x, None, torch.tensor(f, device="cuda"), interleaved=interleaved)
+    t = np.arange(40000)[:, None].astype(np.longdouble) * f.astype(np.longdouble)
+    y = to_f64(y)[0, 0]
+    for got, want in ((y[:, 0::2] if interleaved else y[:, :5], np.cos(t)), (y[:, 1::2] if interleaved else y[:, 5:], np.sin(t))):
+        bound = np.pi * 2.0 ** -27 + 2 * np.pi * 2.0 ** -32 + 2.0 ** -52 * np.abs(t) + np.abs(want) * 2.0 ** -22
+        assert (np.abs(got - want) <= bound).all()
+        # the sine's own two steps apart, the angle's error shows near its zeros
+        near = np.abs(want) < 2.0 ** -6
+        assert near.sum() > 1000 and (np.abs(got - want)[near] <= (bound - np.abs(want) * 2.0 ** -22 + 2.0 ** -28)[near]).all()
