@@ -289,7 +289,8 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
  * (FA_ERR_INVALID).  A sequence length that is negative or beyond max_pages *
  * page_size, and a page number outside 0 .. num_pages - 1, are reported by
  * fa_get_device_status as FA_ERR_INVALID; no memory outside the tensors is
- * touched, and that sequence's results are undefined.
+ * touched, and that sequence's results are undefined.  Zero-initialise a layout:
+ * fields that a call does not use stay 0 / NULL.
  */
 typedef struct {
   int B, H, H_kv, d;
@@ -361,7 +362,8 @@ size_t fa_paged_decode_workspace_size(const fa_paged_layout* layout);
  * Bookkeeping of pages, on the device and without a copy to the host.  The state of a cache is
  *   page_table [num_seqs][max_pages] (rows table_stride apart), seq_lens [num_seqs], refcounts [num_pages],
  * all DEVICE int32: sequence s owns the first ceil(seq_lens[s] / page_size) entries of its row, refcounts
- * counts the rows that hold a page, and a page is free when that is 0.  New pages are the free pages of
+ * counts the rows that hold a page, and a page is free when that is 0.  Lengths grow by fa_pages_extend and fall to 0 by
+ * fa_pages_free; one that is lowered by hand leaves pages held that no call gives back.  New pages are the free pages of
  * lowest number, handed out in the order of the requests, so results do not depend on timing.  A page that is
  * not full belongs to one sequence only.  Calls on one state have to be ordered (one stream).  workspace:
  * fa_pages_workspace_size(layout, n) bytes, 256-byte aligned.
